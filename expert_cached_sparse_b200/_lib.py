@@ -37,8 +37,10 @@ EXPORTS = [
     "moe_layer_forward", "moe_profile_enable", "moe_profile_read", "moe_get_device_error",
     "moe_permute_noalloc", "moe_act_terms", "moe_cache_set_fill_mode", "moe_cache_fill_mode",
     "moe_cache_device_status", "moe_test_set_wait", "moe_prefill_workspace_bytes", "moe_prefill_forward",
+    "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_grouped_gemm_fp8",
+    "moe_fp8_quantize_act", "moe_fp8_quantize_weight",
 ]
-PROF_KINDS = ["router", "lookup", "permute", "ffn", "combine", "fill"]
+PROF_KINDS = ["router", "lookup", "permute", "ffn", "combine", "fill", "gemm", "quant"]
 
 TRACE_DTYPE = np.dtype([("call", "<u4"), ("slot", "<i4"), ("layer", "<u2"), ("expert", "<u2"),
                         ("event", "u1"), ("pad", "u1", 3)])
@@ -68,7 +70,7 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmoe.so not built at {LIB_PATH}: run expert_cached_sparse_b200.build.build()")
     L = C.CDLL(LIB_PATH)
-    P, I32, SZ = C.c_void_p, C.c_int32, C.c_size_t
+    P, I32, I64, SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
     SP = C.POINTER(MoeShape)
     sig = {
         "moe_status_str": (C.c_char_p, [C.c_int]),
@@ -103,6 +105,12 @@ def _load():
         "moe_test_set_wait": (C.c_int, [C.c_int64, I32]),
         "moe_prefill_workspace_bytes": (SZ, [SP, I32]),
         "moe_prefill_forward": (C.c_int, [P, I32, I32, P, I32, P, P, I32, P, P, SZ, P, P, P]),
+        "moe_grouped_gemm": (C.c_int, [I32, I32, I32, P, I64, P, P, I32, P, I64, I32, P]),
+        "moe_grouped_gemm_dx": (C.c_int, [I32, I32, I32, P, I64, P, P, I32, P, I64, I32, P]),
+        "moe_grouped_gemm_dw": (C.c_int, [I32, I32, I32, P, I64, P, I64, P, I32, P, I32, I32, P]),
+        "moe_grouped_gemm_fp8": (C.c_int, [I32, I32, I32, P, I64, P, P, P, P, I32, P, I64, I32, P]),
+        "moe_fp8_quantize_act": (C.c_int, [P, I32, I64, I32, I32, I32, P, I64, P, P]),
+        "moe_fp8_quantize_weight": (C.c_int, [P, I32, I32, I32, I32, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)

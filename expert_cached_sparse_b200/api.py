@@ -239,6 +239,149 @@ def moe_prefill_forward(cache: MoeCache, layer0, xs, wgs, biases, outs, ws, stre
     check("moe_prefill_forward", rc)
 
 
+# ------------------------------------------------------------------ expert matrix products
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _expect(name, t, dtypes, shape):
+    """Raises unless t is a tensor of one of dtypes and of this shape (None: any extent)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        want = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
+        raise ValueError(f"{name} must have shape {want}, got {list(t.shape)}")
+
+
+def _ld(name, t) -> int:
+    """Leading dimension of a row matrix whose columns are adjacent."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be adjacent (strides {t.stride()})")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _packed(name, t) -> None:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_device(**tensors) -> None:
+    """Raises unless every tensor is on the current CUDA device, where the call launches."""
+    for name, t in tensors.items():
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def moe_grouped_gemm(x, w, offsets, y, stream=None):
+    """y[r] = W_e x[r] for the rows [offsets[e], offsets[e+1]) of every expert e.
+
+    x [rows, in] bf16, w [experts, out, in] bf16, offsets int32 [experts + 1], y [rows, out]
+    float32 or bf16; x and y may be column slices of wider matrices."""
+    _expect("w", w, (torch.bfloat16,), (None, None, None))
+    E, N, K = w.shape
+    _expect("x", x, (torch.bfloat16,), (None, K))
+    rows = x.shape[0]
+    _expect("offsets", offsets, (torch.int32,), (E + 1,))
+    _expect("y", y, _FLOATS, (rows, N))
+    ldx, ldy = _ld("x", x), _ld("y", y)
+    _packed("w", w), _packed("offsets", offsets)
+    _on_device(x=x, w=w, offsets=offsets, y=y)
+    rc = L.lib.moe_grouped_gemm(E, K, N, ptr(x), ldx, ptr(w), ptr(offsets), rows, ptr(y), ldy, _dt(y),
+                                stream_handle(stream))
+    check("moe_grouped_gemm", rc)
+
+
+def moe_grouped_gemm_dx(dy, w, offsets, dx, stream=None):
+    """Gradient of moe_grouped_gemm with respect to x: dx[r] = W_e^T dy[r].
+
+    dy [rows, out] bf16, w [experts, out, in] bf16, dx [rows, in] float32 or bf16."""
+    _expect("w", w, (torch.bfloat16,), (None, None, None))
+    E, N, K = w.shape
+    _expect("dy", dy, (torch.bfloat16,), (None, N))
+    rows = dy.shape[0]
+    _expect("offsets", offsets, (torch.int32,), (E + 1,))
+    _expect("dx", dx, _FLOATS, (rows, K))
+    lddy, lddx = _ld("dy", dy), _ld("dx", dx)
+    _packed("w", w), _packed("offsets", offsets)
+    _on_device(dy=dy, w=w, offsets=offsets, dx=dx)
+    rc = L.lib.moe_grouped_gemm_dx(E, K, N, ptr(dy), lddy, ptr(w), ptr(offsets), rows, ptr(dx), lddx, _dt(dx),
+                                   stream_handle(stream))
+    check("moe_grouped_gemm_dx", rc)
+
+
+def moe_grouped_gemm_dw(dy, x, offsets, dw, accumulate=False, stream=None):
+    """Gradient of moe_grouped_gemm with respect to w: dW_e = sum of dy[r] x[r]^T over e's rows.
+
+    dy [rows, out] bf16, x [rows, in] bf16, dw [experts, out, in] float32 or bf16; accumulate
+    adds to what dw holds instead of storing."""
+    _expect("dw", dw, _FLOATS, (None, None, None))
+    E, N, K = dw.shape
+    _expect("dy", dy, (torch.bfloat16,), (None, N))
+    rows = dy.shape[0]
+    _expect("x", x, (torch.bfloat16,), (rows, K))
+    _expect("offsets", offsets, (torch.int32,), (E + 1,))
+    lddy, ldx = _ld("dy", dy), _ld("x", x)
+    _packed("dw", dw), _packed("offsets", offsets)
+    _on_device(dy=dy, x=x, offsets=offsets, dw=dw)
+    rc = L.lib.moe_grouped_gemm_dw(E, K, N, ptr(dy), lddy, ptr(x), ldx, ptr(offsets), rows, ptr(dw), _dt(dw),
+                                   1 if accumulate else 0, stream_handle(stream))
+    check("moe_grouped_gemm_dw", rc)
+
+
+def moe_grouped_gemm_fp8(xq, xs, wq, ws, offsets, y, stream=None):
+    """moe_grouped_gemm of e4m3 codes: xq [rows, in] with scales xs [ceil(in/128), rows], wq
+    [experts, out, in] with scales ws [experts, ceil(out/128), ceil(in/128)] (float32)."""
+    f8 = (torch.float8_e4m3fn,)
+    _expect("wq", wq, f8, (None, None, None))
+    E, N, K = wq.shape
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    _expect("xq", xq, f8, (None, K))
+    rows = xq.shape[0]
+    _expect("xs", xs, (torch.float32,), (kb, rows))
+    _expect("ws", ws, (torch.float32,), (E, nb, kb))
+    _expect("offsets", offsets, (torch.int32,), (E + 1,))
+    _expect("y", y, _FLOATS, (rows, N))
+    ldxq, ldy = _ld("xq", xq), _ld("y", y)
+    _packed("xs", xs), _packed("wq", wq), _packed("ws", ws), _packed("offsets", offsets)
+    _on_device(xq=xq, xs=xs, wq=wq, ws=ws, offsets=offsets, y=y)
+    rc = L.lib.moe_grouped_gemm_fp8(E, K, N, ptr(xq), ldxq, ptr(xs), ptr(wq), ptr(ws), ptr(offsets), rows, ptr(y),
+                                    ldy, _dt(y), stream_handle(stream))
+    check("moe_grouped_gemm_fp8", rc)
+
+
+def moe_fp8_quantize_act(x, q, s, swiglu=False, stream=None):
+    """e4m3 codes q [rows, cols] and scales s [ceil(cols/128), rows] of x [rows, cols] (float32 or
+    bf16), or with swiglu of silu(gate) * up of x [rows, 2 cols] = gate | up."""
+    _expect("q", q, (torch.float8_e4m3fn,), (None, None))
+    rows, cols = q.shape
+    _expect("x", x, _FLOATS, (rows, 2 * cols if swiglu else cols))
+    _expect("s", s, (torch.float32,), ((cols + 127) // 128, rows))
+    ldx, ldq = _ld("x", x), _ld("q", q)
+    _packed("s", s)
+    _on_device(x=x, q=q, s=s)
+    rc = L.lib.moe_fp8_quantize_act(ptr(x), _dt(x), ldx, rows, cols, 1 if swiglu else 0, ptr(q), ldq, ptr(s),
+                                    stream_handle(stream))
+    check("moe_fp8_quantize_act", rc)
+
+
+def moe_fp8_quantize_weight(w, q, s, stream=None):
+    """e4m3 codes q and 128 x 128 block scales s [experts, ceil(out/128), ceil(in/128)] of w
+    [experts, out, in] (float32 or bf16)."""
+    _expect("w", w, _FLOATS, (None, None, None))
+    E, N, K = w.shape
+    _expect("q", q, (torch.float8_e4m3fn,), (E, N, K))
+    _expect("s", s, (torch.float32,), (E, (N + 127) // 128, (K + 127) // 128))
+    _packed("w", w), _packed("q", q), _packed("s", s)
+    _on_device(w=w, q=q, s=s)
+    rc = L.lib.moe_fp8_quantize_weight(ptr(w), _dt(w), E, N, K, ptr(q), ptr(s), stream_handle(stream))
+    check("moe_fp8_quantize_weight", rc)
+
+
 # ------------------------------------------------------------------ testing hooks
 def moe_test_set_wait(cycles: int, withhold: bool = False) -> None:
     """Bounded-wait limit (SM cycles, 0 = default) and stage withholding of later FFN launches."""

@@ -112,7 +112,9 @@ typedef enum {
     MOE_PROF_FFN = 3,     /* grouped FFN kernels (gate-up, down) */
     MOE_PROF_COMBINE = 4, /* combine kernel */
     MOE_PROF_FILL = 5,    /* miss fills: host->device copies, or the device-fill kernel */
-    MOE_PROF_COUNT = 6
+    MOE_PROF_GEMM = 6,    /* expert matrix products and their gradients */
+    MOE_PROF_QUANT = 7,   /* FP8 quantisation kernels */
+    MOE_PROF_COUNT = 8
 } moe_prof_kind;
 
 typedef struct {
@@ -501,6 +503,109 @@ int moe_prefill_forward(moe_cache* cache, int32_t layer0, int32_t n_layers, cons
  */
 int moe_act_terms(const void* d_x, int32_t x_dtype, int32_t rows, int32_t K, int32_t wfmt, int32_t terms,
                   uint8_t* d_codes, uint8_t* d_scales, int32_t* d_row_exp, void* stream);
+
+/* ---------------------------------------------------------------- expert matrix products
+ *
+ * Plain matrix products grouped by expert over row-major matrices, for layers
+ * whose experts are not packed slots: their gradients for training, and an
+ * 8-bit floating-point form with block scales.  Common to the four products:
+ *  - d_offsets [experts+1] (device) are the row ranges moe_permute writes:
+ *    expert e owns rows [offsets[e], offsets[e+1]) of the row matrices, any
+ *    number of them, none included.  A range that is decreasing or does not
+ *    lie inside [0, rows) counts as empty.  Rows that no expert owns are
+ *    neither read into a result nor written: they keep what they held;
+ *  - row matrices have a leading dimension in elements (ld >= width), so a
+ *    column slice of a wider matrix is used in place; weights are packed
+ *    [experts][out][in] row-major (the canonical layout of moe_pack_expert:
+ *    W13 is [2F][H], W2 is [H][F]);
+ *  - 1 <= experts <= 4096; in and out are multiples of 8 (moe_grouped_gemm_fp8:
+ *    in a multiple of 16) up to 2^20; rows up to 2^30; every matrix and the
+ *    leading dimensions of 16-bit and 8-bit ones 16-byte aligned; no output
+ *    may overlap an input;
+ *  - products are summed in fp32 and rounded once to the output type
+ *    (float32 or bf16, nearest even).  The same inputs give the same bits on
+ *    every call.  No workspace, nothing read back: every call can be captured
+ *    in a CUDA graph, and calls on different streams may overlap.
+ * Errors: MOE_ERR_INVALID_ARG for bad sizes, types, alignments or NULL
+ * pointers, MOE_ERR_UNSUPPORTED for sizes above the limits.
+ * Pages: experts found in VRAM execute on the GPU ("FreeToken quantization",
+ * section "Como se desplazan los pesos MoE cuantizados por la memoria"); the
+ * gradients and the FP8 format have no passage.
+ */
+
+/*
+ * y[r] = W_e x[r] for every row r of every expert e.  d_x [rows][in] bf16
+ * (ldx), d_w [experts][out][in] bf16, d_y [rows][out] in y_dtype (ldy).
+ * An expert without rows costs nothing: its weights are not read.
+ */
+int moe_grouped_gemm(int32_t experts, int32_t in, int32_t out, const uint16_t* d_x, int64_t ldx,
+                     const uint16_t* d_w, const int32_t* d_offsets, int32_t rows, void* d_y, int64_t ldy,
+                     int32_t y_dtype, void* stream);
+
+/*
+ * Gradient of moe_grouped_gemm with respect to its rows: dx[r] = W_e^T dy[r].
+ * d_dy [rows][out] bf16 (lddy), d_w as above, d_dx [rows][in] in dx_dtype
+ * (lddx).
+ */
+int moe_grouped_gemm_dx(int32_t experts, int32_t in, int32_t out, const uint16_t* d_dy, int64_t lddy,
+                        const uint16_t* d_w, const int32_t* d_offsets, int32_t rows, void* d_dx, int64_t lddx,
+                        int32_t dx_dtype, void* stream);
+
+/*
+ * Gradient of moe_grouped_gemm with respect to its weights: dW_e = sum over
+ * the rows r of e of dy[r] x[r]^T.  d_dy [rows][out] bf16 (lddy), d_x
+ * [rows][in] bf16 (ldx), d_dw [experts][out][in] in dw_dtype.  accumulate ==
+ * 0 stores the sum (zeros for an expert without rows); otherwise it is added
+ * to what d_dw holds (in fp32, then rounded to dw_dtype), and an expert
+ * without rows is left as it was.  rows may be 0.
+ */
+int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, const uint16_t* d_dy, int64_t lddy,
+                        const uint16_t* d_x, int64_t ldx, const int32_t* d_offsets, int32_t rows, void* d_dw,
+                        int32_t dw_dtype, int32_t accumulate, void* stream);
+
+/*
+ * moe_grouped_gemm with e4m3 codes (OCP FP8: no infinities, S.1111.111 is NaN)
+ * and block scales, as moe_fp8_quantize_act and moe_fp8_quantize_weight write
+ * them:
+ *   y[r][o] = sum over 128-column blocks b of
+ *             (xs[b][r] ws[e][o/128][b]) (sum of xq[r][j] wq[e][o][j] over the block's columns j),
+ * everything in fp32.  d_xq [rows][in] codes (ldxq in elements, a multiple of
+ * 16), d_xs [in/128 rounded up][rows] float32, d_wq [experts][out][in] codes,
+ * d_ws [experts][out/128][in/128] (rounded up) float32, d_y [rows][out] in
+ * y_dtype (ldy).  Scales are any float32 values.  experts == 1 with offsets
+ * {0, rows} is the plain product of one matrix.
+ */
+int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, const uint8_t* d_xq, int64_t ldxq,
+                         const float* d_xs, const uint8_t* d_wq, const float* d_ws, const int32_t* d_offsets,
+                         int32_t rows, void* d_y, int64_t ldy, int32_t y_dtype, void* stream);
+
+/*
+ * Rows -> e4m3 codes with one float32 scale per 128 columns of a row (the
+ * last block may be shorter).  With swiglu == 0 the row is d_x [rows][cols]
+ * (x_dtype, ldx); otherwise d_x is [rows][2 cols], gate then up, and the row
+ * is silu(gate) * up in fp32, not rounded in between.  For a block of
+ * largest magnitude m (NaN left out): s = m / 448, or 1 when m < 2^-100;
+ * q = the e4m3 code nearest to x / s (ties to even), division and quotient in
+ * fp32; codes of a block below 2^-100 are zeros.  A NaN becomes a NaN code;
+ * an infinity makes the block's scale infinite, its own code NaN and the
+ * other codes zero, so every product with that block is NaN.
+ * d_q [rows][cols] codes (ldq), d_s [cols/128 rounded up][rows]: a block
+ * column's scales of consecutive rows are contiguous, as the product reads
+ * them.  cols a multiple of 8 up to 2^20, rows up to 2^30, d_x 16-byte
+ * aligned with 16-byte aligned rows, d_q and ldq multiples of 8 bytes.
+ */
+int moe_fp8_quantize_act(const void* d_x, int32_t x_dtype, int64_t ldx, int32_t rows, int32_t cols, int32_t swiglu,
+                         uint8_t* d_q, int64_t ldq, float* d_s, void* stream);
+
+/*
+ * Weights d_w [experts][out][in] (w_dtype) -> e4m3 codes d_q of the same
+ * shape with one scale per 128 x 128 block of each matrix, d_s
+ * [experts][out/128][in/128] (rounded up); the block's scale and codes by the
+ * rule of moe_fp8_quantize_act.  out >= 1, in a multiple of 8, both up to
+ * 2^20, d_w 16-byte and d_q 8-byte aligned.
+ */
+int moe_fp8_quantize_weight(const void* d_w, int32_t w_dtype, int32_t experts, int32_t out, int32_t in, uint8_t* d_q,
+                            float* d_s, void* stream);
 
 /* ---------------------------------------------------------------- profiling */
 

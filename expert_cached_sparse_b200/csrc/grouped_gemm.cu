@@ -1,128 +1,342 @@
-// Matrix products grouped by expert with ragged row ranges, and their
-// gradients (see include/moe.h).  First form: 64 x 64 output tiles, fp32 FMAs
-// from shared memory, one expert per grid plane.
-#include <cuda_fp8.h>
-
-#include "common.cuh"
+// Matrix products grouped by expert with ragged row ranges, in bf16, and
+// their gradients (see include/moe.h):
+//   FWD  y[r][o]  = sum_i x[r][i] W_e[o][i]
+//   DX   dx[r][i] = sum_o dy[r][o] W_e[o][i]
+//   DW   dW_e[o][i] = sum_r dy[r][o] x[r][i]   over e's rows
+//
+// One kernel, three operand layouts.  A tile is 128 features (the tensor
+// core's M, one tensor-memory lane each: `out` for FWD, `in` for DX and DW) by
+// up to NB columns (N: rows for FWD and DX, `out` for DW), and the inner index
+// advances 64 per pipeline stage.  The features are the operand that is never
+// ragged, so M is always full and N takes any multiple of 16: an expert with
+// one row costs a 128 x 16 tile, not a 128 x 128 one.  TMA brings each operand
+// into the 128-byte swizzle as it lies in memory; where the inner index is
+// not the contiguous one (W in DX, x and dy in DW) the tensor core reads the
+// tile MN-major, so nothing is transposed.  What lies outside a matrix reads
+// as zeros, so odd sizes need no other path.
+//
+// Rows are ragged: in FWD and DX a tile's surplus rows are another expert's
+// (each N column is its own sum; they are not stored).  In DW rows are the
+// inner index, so a last step's surplus rows are zeroed in shared memory, in
+// both operands (a NaN there must not meet a zero), before the MMAs read them.
+//
+// One persistent CTA per SM: warp 0 copies, warp 1 issues the MMAs into one
+// of two accumulators, warps 2-5 read the other one back and store it.  Every
+// wait is bounded; a timeout records MOE_ERR_TIMEOUT, raises the CTA's abort
+// flag so that the other roles stop, and the CTA waits for its own copies and
+// MMAs before it returns.
+#include "tc.cuh"
 
 namespace moe {
+
+__device__ int g_gemm_error;   // first device-side error of the bf16 products (0: none)
+
 namespace {
 
-constexpr int64_t kMaxDim = 1 << 20;
+using namespace tc;
 
-enum Mode { FWD, DX, DW, FP8 };
+constexpr int64_t kMaxDim = 1 << 20;
+constexpr int kThreads = 192;
+constexpr int kMaxStages = 12;
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
+
+enum Mode { FWD, DX, DW };
 
 struct Args {
-    const void* a;          // row matrix: x (FWD, FP8) or dy (DX, DW)
-    int64_t lda;
-    const void* w;          // weights, or x (DW)
-    int64_t ldw;
-    const float* xs;
-    const float* ws;
     const int32_t* offsets;
     void* out;
     int64_t ldo;
-    int out_dtype, accumulate;
-    int experts, in, outs, rows;
+    int out_f32, accumulate;
+    int E, rows;
+    int M, N;        // features; DW: columns (`out`)
+    int K;           // inner size (DW: ragged)
+    int stages;
+    int box;         // rows per copy of the ragged operand (FWD, DX)
+    long long wait;  // limit of every bounded wait, in SM clock cycles
+    int withhold;    // testing: CTA 0 leaves its first stage unfilled
 };
 
-__device__ __forceinline__ float ld_bf16(const void* p, int64_t i)
-{
-    return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-}
-__device__ __forceinline__ float ld_e4m3(const void* p, int64_t i)
-{
-    __nv_fp8_e4m3 v;
-    v.__x = static_cast<const uint8_t*>(p)[i];
-    return (float)v;
-}
+struct Unit {
+    int e, m0, c0, n;   // expert, first feature, first column (row of the matrix, or `out` index), columns
+    int k0, steps;      // DW: first row; steps of 64
+    int tail;           // DW: valid rows of the last step
+};
 
-template <int MODE>
-__global__ void __launch_bounds__(256) gg_kernel(const Args g)
-{
-    __shared__ float sa[16][65], sb[16][65];
-    const int e = blockIdx.z;
-    int r0 = g.offsets[e], r1 = g.offsets[e + 1];
-    if (r0 < 0 || r1 > g.rows || r1 < r0) r0 = r1 = 0;
-    const int m = MODE == DW ? g.outs : r1 - r0;                       // output rows
-    const int n = MODE == FWD || MODE == FP8 ? g.outs : g.in;          // output columns
-    const int kk = MODE == DW ? r1 - r0 : (MODE == DX ? g.outs : g.in);
-    if (MODE == DW && g.accumulate && kk == 0) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int nb = (g.outs + 127) / 128, kb = (g.in + 127) / 128;
-    for (int i0 = blockIdx.y * 64; i0 < m; i0 += gridDim.y * 64)
-        for (int j0 = blockIdx.x * 64; j0 < n; j0 += gridDim.x * 64) {
-            float acc[4][4] = {};
-            for (int k0 = 0; k0 < kk; k0 += 16) {
-                for (int t = threadIdx.x; t < 1024; t += 256) {
-                    const int k = k0 + (t & 15), i = i0 + (t >> 4), j = j0 + (t >> 4);
-                    float va = 0.0f, vb = 0.0f;
-                    if (k < kk && i < m) {
-                        if (MODE == FP8)
-                            va = ld_e4m3(g.a, (int64_t)(r0 + i) * g.lda + k) * g.xs[(int64_t)(k / 128) * g.rows + r0 + i];
-                        else if (MODE == DW)
-                            va = ld_bf16(g.a, (int64_t)(r0 + k) * g.lda + i);
-                        else
-                            va = ld_bf16(g.a, (int64_t)(r0 + i) * g.lda + k);
-                    }
-                    if (k < kk && j < n) {
-                        if (MODE == FP8)
-                            vb = ld_e4m3(g.w, ((int64_t)e * n + j) * kk + k) * g.ws[((int64_t)e * nb + j / 128) * kb + k / 128];
-                        else if (MODE == FWD)
-                            vb = ld_bf16(g.w, ((int64_t)e * n + j) * kk + k);
-                        else if (MODE == DX)
-                            vb = ld_bf16(g.w, ((int64_t)e * kk + k) * n + j);
-                        else
-                            vb = ld_bf16(g.w, (int64_t)(r0 + k) * g.ldw + j);
-                    }
-                    sa[t & 15][t >> 4] = va;
-                    sb[t & 15][t >> 4] = vb;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < 16; k++)
-#pragma unroll
-                    for (int p = 0; p < 4; p++)
-#pragma unroll
-                        for (int q = 0; q < 4; q++) acc[p][q] = fmaf(sa[k][ty * 4 + p], sb[k][tx + 16 * q], acc[p][q]);
-                __syncthreads();
-            }
-            for (int p = 0; p < 4; p++)
-                for (int q = 0; q < 4; q++) {
-                    const int i = i0 + ty * 4 + p, j = j0 + tx + 16 * q;
-                    if (i >= m || j >= n) continue;
-                    const int64_t at = MODE == DW ? ((int64_t)e * m + i) * n + j : (int64_t)(r0 + i) * g.ldo + j;
-                    float v = acc[p][q];
-                    if (g.out_dtype == MOE_DT_F32) {
-                        float* o = static_cast<float*>(g.out) + at;
-                        *o = MODE == DW && g.accumulate ? *o + v : v;
-                    } else {
-                        uint16_t* o = static_cast<uint16_t*>(g.out) + at;
-                        if (MODE == DW && g.accumulate) v += bf16_bits_to_f32(*o);
-                        *o = f32_to_bf16_bits(v);
-                    }
-                }
+// The units of a CTA: u = blockIdx.x, blockIdx.x + gridDim.x, ... .  Row
+// products run through an expert's token blocks fastest, then its feature
+// tiles, so that CTAs running together share weight tiles and rows in L2.
+template <int MODE, int NB>
+struct Units {
+    const Args& a;
+    const LiveExpert* tab;   // FWD, DX
+    const int* off;          // DW: offsets in shared memory
+    int live, mt;
+    long long u, total;
+
+    __device__ Units(const Args& a_, const LiveExpert* t, const int* o, int live_)
+        : a(a_), tab(t), off(o), live(live_), mt((a_.M + 127) / 128), u(blockIdx.x)
+    {
+        if (MODE == DW)
+            total = (long long)a.E * mt * ((a.N + NB - 1) / NB);
+        else
+            total = live ? (long long)tab[live].pre * mt : 0;
+    }
+    __device__ bool next(Unit& v)
+    {
+        if (u >= total) return false;
+        if (MODE == DW) {
+            const int nt = (a.N + NB - 1) / NB, per = mt * nt;
+            const int e = (int)(u / per), r = (int)(u % per);
+            int lo = off[e], hi = off[e + 1];
+            if (lo < 0 || hi < lo || hi > a.rows) lo = hi = 0;
+            v.e = e;
+            v.m0 = (r % mt) * 128;
+            v.c0 = (r / mt) * NB;
+            v.n = min(NB, a.N - v.c0);
+            v.k0 = lo;
+            v.steps = (hi - lo + 63) / 64;
+            v.tail = hi - lo - (v.steps - 1) * 64;
+        } else {
+            const LiveExpert L = tab[find_live(tab, live, mt, u)];
+            const long long r = u - (long long)L.pre * mt;
+            const int nt = (L.r1 - L.r0 + NB - 1) / NB;
+            const int t = (int)(r % nt);
+            v.e = L.e;
+            v.m0 = (int)(r / nt) * 128;
+            v.c0 = L.r0 + t * NB;
+            v.n = min(NB, L.r1 - v.c0);
+            v.k0 = 0;
+            v.steps = (a.K + 63) / 64;
+            v.tail = 64;
         }
+        u += gridDim.x;
+        return true;
+    }
+};
+
+template <int MODE, int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a)
+{
+    constexpr int STAGE = kABytes + NB * 128;
+    constexpr uint32_t TMEM = 2 * NB < 32 ? 32 : 2 * NB;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_scan[2 * kThreads / 32];
+    unsigned char* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    LiveExpert* tab = reinterpret_cast<LiveExpert*>(ring + (size_t)a.stages * STAGE);
+    int* off = reinterpret_cast<int*>(tab);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort_v = &s_abort;
+    int* err = &g_gemm_error;
+
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < a.stages; i++) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&fin), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        tma_prefetch(&tm_a);
+        tma_prefetch(&tm_b);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), TMEM);
+    fence_before();
+    int live = 0;
+    if (MODE == DW) {
+        for (int i = tid; i <= a.E; i += kThreads) off[i] = __ldg(a.offsets + i);
+        __syncthreads();
+    } else {
+        live = build_live(a.offsets, a.E, a.rows, NB, tab, s_scan);
+    }
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    Units<MODE, NB> units(a, tab, off, live);
+    Unit v;
+
+    if (warp == 0) {
+        // ============ copies (the whole warp walks the loop, one elected lane issues)
+        int st = 0, withheld = -1;
+        uint32_t ph = 0;
+        long long issued = 0;
+        bool ok = true;
+        while (ok && units.next(v)) {
+            const int nbox = MODE == DW ? (v.n + 63) / 64 : (v.n + a.box - 1) / a.box;
+            const uint32_t bytes = kABytes + (uint32_t)(MODE == DW ? nbox * 8192 : nbox * a.box * 128);
+            for (int s = 0; s < v.steps; s++) {
+                if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
+                const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
+                if (a.withhold && blockIdx.x == 0 && issued == 0) {
+                    withheld = st;   // testing: never filled, so the wait for it runs out
+                } else {
+                    mbar_expect_tx(bar, bytes);
+                    const int k = v.k0 + 64 * s;
+                    if (MODE == FWD) {
+                        tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
+                    } else if (MODE == DX) {
+                        tma_3d(sa, &tm_a, v.m0, k, v.e, bar);
+                        tma_3d(sa + 8192, &tm_a, v.m0 + 64, k, v.e, bar);
+                    } else {
+                        tma_2d(sa, &tm_a, v.m0, k, bar);
+                        tma_2d(sa + 8192, &tm_a, v.m0 + 64, k, bar);
+                    }
+                    if (MODE == DW)
+                        for (int i = 0; i < nbox; i++) tma_2d(sb + 8192 * i, &tm_b, v.c0 + 64 * i, k, bar);
+                    else
+                        for (int i = 0; i < nbox; i++) tma_2d(sb + 128 * a.box * i, &tm_b, k, v.c0 + a.box * i, bar);
+                }
+                issued++;
+                if (++st == a.stages) { st = 0; ph ^= 1; }
+            }
+        }
+        // every issued copy lands before the CTA exits (stage i was last
+        // filled in this pass over the ring if i < st, else in the previous one)
+        for (int i = 0; i < a.stages && i < issued; i++)
+            if (i != withheld) mbar_drain(smem_u32(&full[i]), i < st ? ph : (ph ^ 1), err);
+    } else if (warp == 1) {
+        // ============ MMAs
+        int st = 0, it = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        while (ok && units.next(v)) {
+            if (v.steps == 0) continue;   // DW: an expert without rows
+            const int ab = it & 1;
+            if (it >= 2) {   // the epilogue has read this accumulator's previous unit
+                if (!(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err))) break;
+                fence_after();
+            }
+            const uint32_t d = tmem + (uint32_t)(ab * NB);
+            const uint32_t id = idesc_bf16((v.n + 15) & ~15, MODE != FWD, MODE == DW);
+            for (int s = 0; s < v.steps; s++) {
+                if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
+                unsigned char* sp = ring + (size_t)st * STAGE;
+                int kk = 4;
+                if (MODE == DW && s == v.steps - 1 && v.tail < 64) {
+                    // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
+                    kk = (v.tail + 15) / 16;
+                    const int z = 16 * kk - v.tail, chunks = 2 + (v.n + 63) / 64;
+                    for (int i = lane; i < z * 8 * chunks; i += 32) {
+                        const int c = i / (z * 8), r = i % (z * 8);
+                        *reinterpret_cast<uint4*>(sp + 8192 * c + 128 * v.tail + 16 * r) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                fence_after();
+                const uint32_t sa = smem_u32(sp), sb = sa + kABytes;
+                const uint64_t da = MODE == FWD ? desc_k(sa) : desc_mn(sa, 8192);
+                const uint64_t db = MODE == DW ? desc_mn(sb, 8192) : desc_k(sb);
+                for (int k = 0; k < kk; k++)   // 16 inner indices: 32 bytes along a K-major row, 16 rows MN-major
+                    mma_bf16(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id, s > 0 || k > 0);
+                commit(smem_u32(&empty[st]));   // the stage is free once these MMAs have read it
+                if (++st == a.stages) { st = 0; ph ^= 1; }
+            }
+            if (!ok) break;
+            commit(smem_u32(&acc_full[ab]));
+            it++;
+        }
+        commit(smem_u32(&fin));   // every MMA completes before tensor memory is released
+        mbar_drain(smem_u32(&fin), 0, err);
+    } else {
+        // ============ epilogue: lane quarter q = warp % 4, one feature per thread.
+        // A warp's store is 32 consecutive features of one column.
+        const int q = warp & 3;
+        int it = 0;
+        bool ok = true;
+        while (ok && units.next(v)) {
+            const int f = v.m0 + 32 * q + lane;
+            const int64_t at = (MODE == DW ? ((int64_t)v.e * a.N + v.c0) : (int64_t)v.c0) * a.ldo + f;
+            float* of = static_cast<float*>(a.out) + at;
+            uint16_t* oh = static_cast<uint16_t*>(a.out) + at;
+            const bool mine = f < a.M;
+            if (MODE == DW && v.steps == 0) {
+                if (mine && !a.accumulate)
+                    for (int c = 0; c < v.n; c++) {
+                        if (a.out_f32) of[c * a.ldo] = 0.0f;
+                        else oh[c * a.ldo] = 0;
+                    }
+                __syncwarp();
+                continue;
+            }
+            const int ab = it & 1;
+            if (!(ok = mbar_wait(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+            fence_after();
+            const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
+            for (int c0 = 0; c0 < v.n; c0 += 16) {
+                uint32_t d[16];
+                tmem_ld16(src + c0, d);
+                wait_ld();
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        if (c0 + j >= v.n) break;
+                        float x = __uint_as_float(d[j]);
+                        const int64_t o = (int64_t)(c0 + j) * a.ldo;
+                        if (a.out_f32) {
+                            if (MODE == DW && a.accumulate) x += of[o];
+                            of[o] = x;
+                        } else {
+                            if (MODE == DW && a.accumulate) x += bf16_bits_to_f32(oh[o]);
+                            oh[o] = f32_to_bf16_bits(x);
+                        }
+                    }
+                }
+                __syncwarp();   // the warp's next tensor-memory load is a converged one
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+            it++;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc(tmem, TMEM);
+    }
 }
 
-template <int MODE>
-int launch(const Args& g, void* stream)
+int device_sms(int* sms)
 {
-    cudaStream_t st = as_stream(stream);
+    int dev = 0;
+    MOE_CUDA_TRY(cudaGetDevice(&dev));
+    MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+    return MOE_OK;
+}
+
+template <int MODE, int NB>
+int launch_nb(Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
+{
+    constexpr int STAGE = kABytes + NB * 128;
+    int sms = 0;
+    if (int rc = device_sms(&sms)) return rc;
+    const int table = (int)align_up(MODE == DW ? sizeof(int) * (a.E + 1) : sizeof(LiveExpert) * (a.E + 1), 128);
+    a.stages = (kSmemMax - 2048 - table) / STAGE;   // 1 KB static, 1 KB alignment slack
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    const int smem = 1024 + a.stages * STAGE + table;
+    auto* kern = gg_kernel<MODE, NB>;
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    const int m = MODE == DW ? g.outs : g.rows, n = MODE == FWD || MODE == FP8 ? g.outs : g.in;
-    const int gx = (n + 63) / 64, gy = (m + 63) / 64;
-    const dim3 grid(gx < 64 ? gx : 64, gy < 16 ? gy : 16, g.experts);
-    gg_kernel<MODE><<<grid, 256, 0, st>>>(g);
+    kern<<<sms, kThreads, smem, st>>>(ta, tb, a);
     MOE_LAUNCH_CHECK();
     return MOE_OK;
 }
 
 // Checks common to the products; MOE_OK to go on.
-int check_sizes(int experts, int in, int out, int rows, int in_mult)
+int check_sizes(int experts, int in, int out, int rows)
 {
-    if (experts <= 0 || in <= 0 || in % in_mult || out <= 0 || out % 8 || rows < 0) return MOE_ERR_INVALID_ARG;
+    if (experts <= 0 || in <= 0 || in % 8 || out <= 0 || out % 8 || rows < 0) return MOE_ERR_INVALID_ARG;
     if (experts > kMaxExperts || in > kMaxDim || out > kMaxDim || rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -134,7 +348,78 @@ bool rows_ok(const void* p, int64_t ld, int64_t width, int size)
 bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_BF16; }
 int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
 
+bool map_rows(CUtensorMap* m, const void* p, int64_t ld, int width, int rows, int box)
+{
+    const uint64_t dims[2] = {(uint64_t)width, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
+    const uint32_t b[2] = {64, (uint32_t)box};
+    return encode_map(m, false, 2, p, dims, strides, b);
+}
+
+// Products of rows with weights: y = x W^T (FWD) or dx = dy W (DX).
+template <int MODE>
+int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets,
+                int rows, void* y, int64_t ldy, int y_dtype, void* stream)
+{
+    Args a{};
+    a.offsets = offsets;
+    a.out = y;
+    a.ldo = ldy;
+    a.out_f32 = y_dtype == MOE_DT_F32;
+    a.E = E;
+    a.rows = rows;
+    a.M = MODE == FWD ? out : in;
+    a.K = MODE == FWD ? in : out;
+    a.wait = test_wait_cycles(kWaitCycles);
+    a.withhold = test_withhold();
+    CUtensorMap ta, tb;
+    const uint64_t dims[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)E};
+    const uint64_t strides[2] = {(uint64_t)in * 2, (uint64_t)in * out * 2};
+    const uint32_t box[3] = {64, MODE == FWD ? 128u : 64u, 1};
+    const bool small = rows <= 16 * (int64_t)E;
+    a.box = small ? 16 : 64;
+    if (!encode_map(&ta, false, 3, w, dims, strides, box) || !map_rows(&tb, x, ldx, a.K, rows, a.box)) return MOE_ERR_CUDA;
+    cudaStream_t st = as_stream(stream);
+    return small ? launch_nb<MODE, 32>(a, ta, tb, st) : launch_nb<MODE, 256>(a, ta, tb, st);
+}
+
 }  // namespace
+
+int gemm_device_error(int clear)
+{
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gemm_error, sizeof v) != cudaSuccess) return MOE_ERR_CUDA;
+    if (clear && v) {
+        const int z = 0;
+        if (cudaMemcpyToSymbol(g_gemm_error, &z, sizeof z) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return v;
+}
+
+namespace tc {
+
+bool encode_map(CUtensorMap* m, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box)
+{
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                  const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tc
 }  // namespace moe
 
 using namespace moe;
@@ -143,52 +428,53 @@ extern "C" int moe_grouped_gemm(int32_t experts, int32_t in, int32_t out, const 
                                 const uint16_t* d_w, const int32_t* d_offsets, int32_t rows, void* d_y, int64_t ldy,
                                 int32_t y_dtype, void* stream)
 {
-    if (int rc = check_sizes(experts, in, out, rows, 8)) return rc;
+    if (int rc = check_sizes(experts, in, out, rows)) return rc;
     if (!out_dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!d_offsets || !rows_ok(d_x, ldx, in, 2) || !rows_ok(d_w, in, in, 2) || !rows_ok(d_y, ldy, out, dtype_size(y_dtype)))
         return MOE_ERR_INVALID_ARG;
-    return launch<FWD>({d_x, ldx, d_w, in, nullptr, nullptr, d_offsets, d_y, ldy, y_dtype, 0, experts, in, out, rows},
-                       stream);
+    return row_product<FWD>(experts, in, out, d_x, ldx, d_w, d_offsets, rows, d_y, ldy, y_dtype, stream);
 }
 
 extern "C" int moe_grouped_gemm_dx(int32_t experts, int32_t in, int32_t out, const uint16_t* d_dy, int64_t lddy,
                                    const uint16_t* d_w, const int32_t* d_offsets, int32_t rows, void* d_dx,
                                    int64_t lddx, int32_t dx_dtype, void* stream)
 {
-    if (int rc = check_sizes(experts, in, out, rows, 8)) return rc;
+    if (int rc = check_sizes(experts, in, out, rows)) return rc;
     if (!out_dtype_ok(dx_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!d_offsets || !rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_w, in, in, 2) ||
         !rows_ok(d_dx, lddx, in, dtype_size(dx_dtype)))
         return MOE_ERR_INVALID_ARG;
-    return launch<DX>({d_dy, lddy, d_w, in, nullptr, nullptr, d_offsets, d_dx, lddx, dx_dtype, 0, experts, in, out, rows},
-                      stream);
+    return row_product<DX>(experts, in, out, d_dy, lddy, d_w, d_offsets, rows, d_dx, lddx, dx_dtype, stream);
 }
 
 extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, const uint16_t* d_dy, int64_t lddy,
                                    const uint16_t* d_x, int64_t ldx, const int32_t* d_offsets, int32_t rows,
                                    void* d_dw, int32_t dw_dtype, int32_t accumulate, void* stream)
 {
-    if (int rc = check_sizes(experts, in, out, rows, 8)) return rc;
+    if (int rc = check_sizes(experts, in, out, rows)) return rc;
     if (!out_dtype_ok(dw_dtype) || !d_offsets || !rows_ok(d_dw, in, in, dtype_size(dw_dtype))) return MOE_ERR_INVALID_ARG;
     if (rows > 0 && (!rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_x, ldx, in, 2))) return MOE_ERR_INVALID_ARG;
-    return launch<DW>({d_dy, lddy, d_x, ldx, nullptr, nullptr, d_offsets, d_dw, in, dw_dtype, accumulate ? 1 : 0, experts,
-                       in, out, rows},
-                      stream);
-}
-
-extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, const uint8_t* d_xq, int64_t ldxq,
-                                    const float* d_xs, const uint8_t* d_wq, const float* d_ws,
-                                    const int32_t* d_offsets, int32_t rows, void* d_y, int64_t ldy, int32_t y_dtype,
-                                    void* stream)
-{
-    if (int rc = check_sizes(experts, in, out, rows, 16)) return rc;
-    if (!out_dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
-    if (rows == 0) return MOE_OK;
-    if (!d_offsets || !d_xs || !d_ws || ((uintptr_t)d_xs & 3) || ((uintptr_t)d_ws & 3) || !rows_ok(d_xq, ldxq, in, 1) ||
-        !rows_ok(d_wq, in, in, 1) || !rows_ok(d_y, ldy, out, dtype_size(y_dtype)))
-        return MOE_ERR_INVALID_ARG;
-    return launch<FP8>({d_xq, ldxq, d_wq, in, d_xs, d_ws, d_offsets, d_y, ldy, y_dtype, 0, experts, in, out, rows},
-                       stream);
+    cudaStream_t st = as_stream(stream);
+    if (rows == 0) {
+        if (!accumulate)
+            MOE_CUDA_TRY(cudaMemsetAsync(d_dw, 0, (size_t)experts * out * in * dtype_size(dw_dtype), st));
+        return MOE_OK;
+    }
+    Args a{};
+    a.offsets = d_offsets;
+    a.out = d_dw;
+    a.ldo = in;
+    a.out_f32 = dw_dtype == MOE_DT_F32;
+    a.accumulate = accumulate ? 1 : 0;
+    a.E = experts;
+    a.rows = rows;
+    a.M = in;
+    a.N = out;
+    a.wait = test_wait_cycles(kWaitCycles);
+    a.withhold = test_withhold();
+    CUtensorMap ta, tb;
+    if (!map_rows(&ta, d_x, ldx, in, rows, 64) || !map_rows(&tb, d_dy, lddy, out, rows, 64)) return MOE_ERR_CUDA;
+    return launch_nb<DW, 256>(a, ta, tb, st);
 }

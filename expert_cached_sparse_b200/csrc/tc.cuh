@@ -1,0 +1,247 @@
+// Tensor-core (tcgen05), TMA and mbarrier wrappers of the expert matrix
+// products (grouped_gemm.cu, grouped_gemm_fp8.cu).  The issuing wrappers are
+// called by converged warps: every lane computes the operands, one lane
+// elected by elect.sync issues.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace tc {
+
+constexpr long long kWaitCycles = 4000000000ll;   // ~2 s: drains, and waits unless a test sets a limit
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// ------------------------------------------------------------------ mbarriers
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// One arrival by the calling lane.
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "n"(20000)
+                 : "memory");
+    return ok != 0;
+}
+// Bounded wait of a whole warp: false when another role raised the abort
+// flag, or after `limit` cycles, in which case it raises the flag itself and
+// records MOE_ERR_TIMEOUT in *error.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit,
+                                          int* error)
+{
+    bool ok = mbar_try(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = mbar_try(bar, parity))) {
+            if (*abort_flag) break;
+            if (clock64() - t0 > limit) {
+                *abort_flag = 1;
+                atomicCAS(error, 0, (int)MOE_ERR_TIMEOUT);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+// Drain wait for this CTA's own copies or MMAs before it exits: bounded by
+// time only.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, int* error)
+{
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity))
+        if (clock64() - t0 > kWaitCycles) {
+            atomicCAS(error, 0, (int)MOE_ERR_TIMEOUT);
+            return;
+        }
+}
+
+// ------------------------------------------------------------------ TMA
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+                 : "memory");
+}
+// `cols` (a power of two >= 32) tensor-memory columns; the address lands in *slot.
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+// Shared-memory descriptors in the 128-byte swizzle.  K-major: rows of 128
+// bytes (one row per M or N index), 8-row groups 1024 bytes apart.  MN-major:
+// rows of 128 bytes (64 16-bit M or N indices) per K index, 8-row groups 1024
+// bytes apart, the next 64 M or N indices `chunk` bytes on.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t chunk)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor, fp32 accumulators, M = 128, N = n (a multiple of
+// 16): bf16 operands (kind::f16) with either operand MN-major, or e4m3
+// (kind::f8f6f4, K-major, every format field 0).
+__device__ __forceinline__ uint32_t idesc_bf16(int n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
+
+// D[tmem] (+)= A[smem] B[smem], K = 16 bf16 or 32 e4m3 columns.
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// 16 consecutive columns of the warp's 32 lanes (32 * (warp % 4) on).
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+                 "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+                   "=r"(v[15])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ host: tensor maps
+// A row-major tensor of `rank` dimensions (dims[0] innermost), strides in
+// bytes of dims 1.., copied in boxes whose inner extent is 128 bytes and
+// stored in the 128-byte swizzle.  Reads outside the tensor give zeros.
+// False when the driver refuses it.
+bool encode_map(CUtensorMap* m, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box);
+
+}  // namespace tc
+
+// ------------------------------------------------------------------ units of the row-grouped products
+// One live expert: the token blocks before its first one, its id and rows.
+struct LiveExpert {
+    int pre, e, r0, r1;
+};
+
+// The call's live experts in ascending order, in shared memory, with one
+// closing entry {total token blocks}; NB rows per token block.  Called by all
+// threads of the CTA; `scratch` holds 2 ints per warp.  Returns how many.
+// Ranges that no offsets of moe_permute would hold count as empty; ranges
+// that overlap so often that the blocks pass 2^31 void the whole call.
+__device__ __forceinline__ int build_live(const int32_t* __restrict__ offsets, int E, int rows, int NB,
+                                          LiveExpert* tab, int* scratch)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int per = (E + nt - 1) / nt;
+    const int e0 = tid * per, e1 = min(E, e0 + per);
+    int n = 0;
+    long long b = 0;
+    for (int e = e0; e < e1; e++) {
+        const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
+        if (lo >= 0 && hi > lo && hi <= rows) {
+            n++;
+            b += (hi - lo + NB - 1) / NB;
+        }
+    }
+    int ni = n;
+    long long bi = b;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int nn = __shfl_up_sync(0xffffffffu, ni, o);
+        const long long bb = __shfl_up_sync(0xffffffffu, bi, o);
+        if (lane >= o) { ni += nn; bi += bb; }
+    }
+    if (lane == 31) {
+        scratch[2 * warp] = ni;
+        scratch[2 * warp + 1] = (int)min(bi, (long long)0x7fffffff);
+    }
+    __syncthreads();
+    int live = 0, nb = ni - n;
+    long long total = 0, base = bi - b;
+    for (int w = 0; w < nt / 32; w++) {
+        if (w < warp) { nb += scratch[2 * w]; base += scratch[2 * w + 1]; }
+        live += scratch[2 * w];
+        total += scratch[2 * w + 1];
+    }
+    if (total >= 0x7fffffff) live = 0;
+    else
+        for (int e = e0; e < e1; e++) {
+            const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
+            if (lo >= 0 && hi > lo && hi <= rows) {
+                tab[nb++] = {(int)base, e, lo, hi};
+                base += (hi - lo + NB - 1) / NB;
+            }
+        }
+    if (tid == 0) tab[live] = {live ? (int)total : 0, 0, 0, 0};
+    __syncthreads();
+    return live;
+}
+
+// Index of the live expert that unit u (mt feature tiles per token block) belongs to.
+__device__ __forceinline__ int find_live(const LiveExpert* tab, int live, int mt, long long u)
+{
+    int lo = 0, hi = live - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)tab[mid].pre * mt <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace moe

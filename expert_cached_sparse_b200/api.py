@@ -240,41 +240,53 @@ def moe_prefill_forward(cache: MoeCache, layer0, xs, wgs, biases, outs, ws, stre
 
 
 # ------------------------------------------------------------------ expert matrix products
-_FLOATS = (torch.float32, torch.bfloat16)
+# These calls are short next to a Python check per argument, so the checks of a
+# call are a few comparisons; _refuse works out which one failed.
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+_OUT = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 
 
-def _expect(name, t, dtypes, shape):
-    """Raises unless t is a tensor of one of dtypes and of this shape (None: any extent)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-        want = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
-        raise ValueError(f"{name} must have shape {want}, got {list(t.shape)}")
+def _refuse(fn, **specs):
+    """Raises the error of the first argument that is not as required: name = (tensor, dtypes, shape,
+    packed), None in a shape for any extent."""
+    for name, (t, dtypes, shape, packed) in specs.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{fn}: {name} must be a torch tensor, got {type(t).__name__}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            want = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
+            raise ValueError(f"{fn}: {name} must have shape {want}, got {list(t.shape)}")
+        if packed and not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+        if not packed and _ld(t) < 0:
+            raise ValueError(f"{fn}: {name} must have adjacent columns and rows that do not overlap, got strides {t.stride()}")
+    for name, (t, *_) in specs.items():
+        if t.get_device() != _device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+    raise AssertionError(fn)
 
 
-def _ld(name, t) -> int:
-    """Leading dimension of a row matrix whose columns are adjacent."""
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: columns must be adjacent (strides {t.stride()})")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.stride(0)
+def _ld(t) -> int:
+    """Leading dimension of a row matrix whose columns are adjacent, -1 of any other."""
+    rows, cols = t.shape
+    a, b = t.stride()
+    if b != 1 and cols > 1:
+        return -1
+    return cols if rows <= 1 else a if a >= cols else -1
 
 
-def _packed(name, t) -> None:
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _dims(*pairs) -> bool:
+    """Whether every (argument, dimensions) is a tensor of that many dimensions."""
+    for t, d in pairs:
+        if not isinstance(t, torch.Tensor) or t.dim() != d:
+            return False
+    return True
 
 
-def _on_device(**tensors) -> None:
-    """Raises unless every tensor is on the current CUDA device, where the call launches."""
-    for name, t in tensors.items():
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+def _device() -> int:
+    """The current CUDA device, where the calls launch; -2 (no tensor's) without one."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
 def moe_grouped_gemm(x, w, offsets, y, stream=None):
@@ -282,17 +294,17 @@ def moe_grouped_gemm(x, w, offsets, y, stream=None):
 
     x [rows, in] bf16, w [experts, out, in] bf16, offsets int32 [experts + 1], y [rows, out]
     float32 or bf16; x and y may be column slices of wider matrices."""
-    _expect("w", w, (torch.bfloat16,), (None, None, None))
-    E, N, K = w.shape
-    _expect("x", x, (torch.bfloat16,), (None, K))
-    rows = x.shape[0]
-    _expect("offsets", offsets, (torch.int32,), (E + 1,))
-    _expect("y", y, _FLOATS, (rows, N))
-    ldx, ldy = _ld("x", x), _ld("y", y)
-    _packed("w", w), _packed("offsets", offsets)
-    _on_device(x=x, w=w, offsets=offsets, y=y)
-    rc = L.lib.moe_grouped_gemm(E, K, N, ptr(x), ldx, ptr(w), ptr(offsets), rows, ptr(y), ldy, _dt(y),
-                                stream_handle(stream))
+    E, N, K = w.shape if _dims((w, 3)) else (None, None, None)
+    rows = x.shape[0] if _dims((x, 2)) else None
+    if not (_dims((offsets, 1), (y, 2)) and E is not None and rows is not None
+            and x.dtype is _BF16 and w.dtype is _BF16 and offsets.dtype is _I32 and y.dtype in _OUT
+            and x.shape[1] == K and offsets.shape[0] == E + 1 and y.shape == (rows, N)
+            and w.is_contiguous() and offsets.is_contiguous() and (ldx := _ld(x)) >= 0 and (ldy := _ld(y)) >= 0
+            and x.get_device() == w.get_device() == offsets.get_device() == y.get_device() == _device()):
+        _refuse("moe_grouped_gemm", w=(w, (_BF16,), (None, None, None), True), x=(x, (_BF16,), (None, K), False),
+                offsets=(offsets, (_I32,), (E and E + 1,), True), y=(y, _OUT, (rows, N), False))
+    rc = L.lib.moe_grouped_gemm(E, K, N, x.data_ptr(), ldx, w.data_ptr(), offsets.data_ptr(), rows, y.data_ptr(), ldy,
+                                _OUT[y.dtype], stream_handle(stream))
     check("moe_grouped_gemm", rc)
 
 
@@ -300,17 +312,17 @@ def moe_grouped_gemm_dx(dy, w, offsets, dx, stream=None):
     """Gradient of moe_grouped_gemm with respect to x: dx[r] = W_e^T dy[r].
 
     dy [rows, out] bf16, w [experts, out, in] bf16, dx [rows, in] float32 or bf16."""
-    _expect("w", w, (torch.bfloat16,), (None, None, None))
-    E, N, K = w.shape
-    _expect("dy", dy, (torch.bfloat16,), (None, N))
-    rows = dy.shape[0]
-    _expect("offsets", offsets, (torch.int32,), (E + 1,))
-    _expect("dx", dx, _FLOATS, (rows, K))
-    lddy, lddx = _ld("dy", dy), _ld("dx", dx)
-    _packed("w", w), _packed("offsets", offsets)
-    _on_device(dy=dy, w=w, offsets=offsets, dx=dx)
-    rc = L.lib.moe_grouped_gemm_dx(E, K, N, ptr(dy), lddy, ptr(w), ptr(offsets), rows, ptr(dx), lddx, _dt(dx),
-                                   stream_handle(stream))
+    E, N, K = w.shape if _dims((w, 3)) else (None, None, None)
+    rows = dy.shape[0] if _dims((dy, 2)) else None
+    if not (_dims((offsets, 1), (dx, 2)) and E is not None and rows is not None
+            and dy.dtype is _BF16 and w.dtype is _BF16 and offsets.dtype is _I32 and dx.dtype in _OUT
+            and dy.shape[1] == N and offsets.shape[0] == E + 1 and dx.shape == (rows, K)
+            and w.is_contiguous() and offsets.is_contiguous() and (lddy := _ld(dy)) >= 0 and (lddx := _ld(dx)) >= 0
+            and dy.get_device() == w.get_device() == offsets.get_device() == dx.get_device() == _device()):
+        _refuse("moe_grouped_gemm_dx", w=(w, (_BF16,), (None, None, None), True), dy=(dy, (_BF16,), (None, N), False),
+                offsets=(offsets, (_I32,), (E and E + 1,), True), dx=(dx, _OUT, (rows, K), False))
+    rc = L.lib.moe_grouped_gemm_dx(E, K, N, dy.data_ptr(), lddy, w.data_ptr(), offsets.data_ptr(), rows, dx.data_ptr(),
+                                   lddx, _OUT[dx.dtype], stream_handle(stream))
     check("moe_grouped_gemm_dx", rc)
 
 
@@ -319,66 +331,71 @@ def moe_grouped_gemm_dw(dy, x, offsets, dw, accumulate=False, stream=None):
 
     dy [rows, out] bf16, x [rows, in] bf16, dw [experts, out, in] float32 or bf16; accumulate
     adds to what dw holds instead of storing."""
-    _expect("dw", dw, _FLOATS, (None, None, None))
-    E, N, K = dw.shape
-    _expect("dy", dy, (torch.bfloat16,), (None, N))
-    rows = dy.shape[0]
-    _expect("x", x, (torch.bfloat16,), (rows, K))
-    _expect("offsets", offsets, (torch.int32,), (E + 1,))
-    lddy, ldx = _ld("dy", dy), _ld("x", x)
-    _packed("dw", dw), _packed("offsets", offsets)
-    _on_device(dy=dy, x=x, offsets=offsets, dw=dw)
-    rc = L.lib.moe_grouped_gemm_dw(E, K, N, ptr(dy), lddy, ptr(x), ldx, ptr(offsets), rows, ptr(dw), _dt(dw),
-                                   1 if accumulate else 0, stream_handle(stream))
+    E, N, K = dw.shape if _dims((dw, 3)) else (None, None, None)
+    rows = dy.shape[0] if _dims((dy, 2)) else None
+    if not (_dims((offsets, 1), (x, 2)) and E is not None and rows is not None
+            and dy.dtype is _BF16 and x.dtype is _BF16 and offsets.dtype is _I32 and dw.dtype in _OUT
+            and dy.shape[1] == N and x.shape == (rows, K) and offsets.shape[0] == E + 1
+            and dw.is_contiguous() and offsets.is_contiguous() and (lddy := _ld(dy)) >= 0 and (ldx := _ld(x)) >= 0
+            and dy.get_device() == x.get_device() == offsets.get_device() == dw.get_device() == _device()):
+        _refuse("moe_grouped_gemm_dw", dw=(dw, _OUT, (None, None, None), True), dy=(dy, (_BF16,), (None, N), False),
+                x=(x, (_BF16,), (rows, K), False), offsets=(offsets, (_I32,), (E and E + 1,), True))
+    rc = L.lib.moe_grouped_gemm_dw(E, K, N, dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows,
+                                   dw.data_ptr(), _OUT[dw.dtype], 1 if accumulate else 0, stream_handle(stream))
     check("moe_grouped_gemm_dw", rc)
 
 
 def moe_grouped_gemm_fp8(xq, xs, wq, ws, offsets, y, stream=None):
     """moe_grouped_gemm of e4m3 codes: xq [rows, in] with scales xs [ceil(in/128), rows], wq
     [experts, out, in] with scales ws [experts, ceil(out/128), ceil(in/128)] (float32)."""
-    f8 = (torch.float8_e4m3fn,)
-    _expect("wq", wq, f8, (None, None, None))
-    E, N, K = wq.shape
-    nb, kb = (N + 127) // 128, (K + 127) // 128
-    _expect("xq", xq, f8, (None, K))
-    rows = xq.shape[0]
-    _expect("xs", xs, (torch.float32,), (kb, rows))
-    _expect("ws", ws, (torch.float32,), (E, nb, kb))
-    _expect("offsets", offsets, (torch.int32,), (E + 1,))
-    _expect("y", y, _FLOATS, (rows, N))
-    ldxq, ldy = _ld("xq", xq), _ld("y", y)
-    _packed("xs", xs), _packed("wq", wq), _packed("ws", ws), _packed("offsets", offsets)
-    _on_device(xq=xq, xs=xs, wq=wq, ws=ws, offsets=offsets, y=y)
-    rc = L.lib.moe_grouped_gemm_fp8(E, K, N, ptr(xq), ldxq, ptr(xs), ptr(wq), ptr(ws), ptr(offsets), rows, ptr(y),
-                                    ldy, _dt(y), stream_handle(stream))
+    E, N, K = wq.shape if _dims((wq, 3)) else (None, None, None)
+    rows = xq.shape[0] if _dims((xq, 2)) else None
+    nb, kb = (None, None) if E is None else ((N + 127) // 128, (K + 127) // 128)
+    if not (_dims((xs, 2), (ws, 3), (offsets, 1), (y, 2)) and E is not None and rows is not None
+            and xq.dtype is _E4M3 and wq.dtype is _E4M3 and xs.dtype is _F32 and ws.dtype is _F32
+            and offsets.dtype is _I32 and y.dtype in _OUT and xq.shape[1] == K and xs.shape == (kb, rows)
+            and ws.shape == (E, nb, kb) and offsets.shape[0] == E + 1 and y.shape == (rows, N)
+            and xs.is_contiguous() and wq.is_contiguous() and ws.is_contiguous() and offsets.is_contiguous()
+            and (ldxq := _ld(xq)) >= 0 and (ldy := _ld(y)) >= 0
+            and xq.get_device() == xs.get_device() == wq.get_device() == ws.get_device() == offsets.get_device()
+            == y.get_device() == _device()):
+        _refuse("moe_grouped_gemm_fp8", wq=(wq, (_E4M3,), (None, None, None), True), xq=(xq, (_E4M3,), (None, K), False),
+                xs=(xs, (_F32,), (kb, rows), True), ws=(ws, (_F32,), (E, nb, kb), True),
+                offsets=(offsets, (_I32,), (E and E + 1,), True), y=(y, _OUT, (rows, N), False))
+    rc = L.lib.moe_grouped_gemm_fp8(E, K, N, xq.data_ptr(), ldxq, xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+                                    offsets.data_ptr(), rows, y.data_ptr(), ldy, _OUT[y.dtype], stream_handle(stream))
     check("moe_grouped_gemm_fp8", rc)
 
 
 def moe_fp8_quantize_act(x, q, s, swiglu=False, stream=None):
     """e4m3 codes q [rows, cols] and scales s [ceil(cols/128), rows] of x [rows, cols] (float32 or
     bf16), or with swiglu of silu(gate) * up of x [rows, 2 cols] = gate | up."""
-    _expect("q", q, (torch.float8_e4m3fn,), (None, None))
-    rows, cols = q.shape
-    _expect("x", x, _FLOATS, (rows, 2 * cols if swiglu else cols))
-    _expect("s", s, (torch.float32,), ((cols + 127) // 128, rows))
-    ldx, ldq = _ld("x", x), _ld("q", q)
-    _packed("s", s)
-    _on_device(x=x, q=q, s=s)
-    rc = L.lib.moe_fp8_quantize_act(ptr(x), _dt(x), ldx, rows, cols, 1 if swiglu else 0, ptr(q), ldq, ptr(s),
-                                    stream_handle(stream))
+    rows, cols = q.shape if _dims((q, 2)) else (None, None)
+    width, kb = (None, None) if cols is None else (2 * cols if swiglu else cols, (cols + 127) // 128)
+    if not (_dims((x, 2), (s, 2)) and cols is not None and q.dtype is _E4M3 and x.dtype in _OUT and s.dtype is _F32
+            and x.shape == (rows, width) and s.shape == (kb, rows) and s.is_contiguous()
+            and (ldx := _ld(x)) >= 0 and (ldq := _ld(q)) >= 0
+            and x.get_device() == q.get_device() == s.get_device() == _device()):
+        _refuse("moe_fp8_quantize_act", q=(q, (_E4M3,), (None, None), False), x=(x, _OUT, (rows, width), False),
+                s=(s, (_F32,), (kb, rows), True))
+    rc = L.lib.moe_fp8_quantize_act(x.data_ptr(), _OUT[x.dtype], ldx, rows, cols, 1 if swiglu else 0, q.data_ptr(), ldq,
+                                    s.data_ptr(), stream_handle(stream))
     check("moe_fp8_quantize_act", rc)
 
 
 def moe_fp8_quantize_weight(w, q, s, stream=None):
     """e4m3 codes q and 128 x 128 block scales s [experts, ceil(out/128), ceil(in/128)] of w
     [experts, out, in] (float32 or bf16)."""
-    _expect("w", w, _FLOATS, (None, None, None))
-    E, N, K = w.shape
-    _expect("q", q, (torch.float8_e4m3fn,), (E, N, K))
-    _expect("s", s, (torch.float32,), (E, (N + 127) // 128, (K + 127) // 128))
-    _packed("w", w), _packed("q", q), _packed("s", s)
-    _on_device(w=w, q=q, s=s)
-    rc = L.lib.moe_fp8_quantize_weight(ptr(w), _dt(w), E, N, K, ptr(q), ptr(s), stream_handle(stream))
+    E, N, K = w.shape if _dims((w, 3)) else (None, None, None)
+    nb, kb = (None, None) if E is None else ((N + 127) // 128, (K + 127) // 128)
+    if not (_dims((q, 3), (s, 3)) and E is not None and w.dtype in _OUT and q.dtype is _E4M3 and s.dtype is _F32
+            and q.shape == (E, N, K) and s.shape == (E, nb, kb)
+            and w.is_contiguous() and q.is_contiguous() and s.is_contiguous()
+            and w.get_device() == q.get_device() == s.get_device() == _device()):
+        _refuse("moe_fp8_quantize_weight", w=(w, _OUT, (None, None, None), True), q=(q, (_E4M3,), (E, N, K), True),
+                s=(s, (_F32,), (E, nb, kb), True))
+    rc = L.lib.moe_fp8_quantize_weight(w.data_ptr(), _OUT[w.dtype], E, N, K, q.data_ptr(), s.data_ptr(),
+                                       stream_handle(stream))
     check("moe_fp8_quantize_weight", rc)
 
 

@@ -171,6 +171,7 @@ long long test_wait_cycles(long long dflt);
 int test_withhold();
 int ffn_fp4_device_error(int clear);   // FP4 FFN's device error word (0: none)
 int gemm_device_error(int clear);      // bf16 expert products' device error word (0: none)
+int gemm8_device_error(int clear);     // FP8 expert products' device error word (0: none)
 // one_expert: the pass computes at most one expert (a miss group after the
 // first), so the FP4 decode tiles run on a grid sized for one expert's work.
 int launch_ffn(const moe_shape* s, const void* pool, size_t slot_bytes, int pool_slots, const int32_t* slot_of,

@@ -771,6 +771,7 @@ extern "C" int moe_get_device_error(int clear)
     const int a = moe::ffn_fp4_device_error(clear);
     const int b = moe::ffn_device_error(clear);
     const int c = moe::gemm_device_error(clear);
+    const int d = moe::gemm8_device_error(clear);
     if (a < 0 && a != MOE_ERR_TIMEOUT) return a;   // the read itself failed
-    return a ? a : b ? b : c;
+    return a ? a : b ? b : c ? c : d;
 }

@@ -35,10 +35,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int64_t kMaxDim = 1 << 20;
 constexpr int kThreads = 192;
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 227 * 1024;
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
 
 enum Mode { FWD, DX, DW };
@@ -63,30 +61,24 @@ struct Unit {
     int tail;           // DW: valid rows of the last step
 };
 
-// The units of a CTA: u = blockIdx.x, blockIdx.x + gridDim.x, ... .  Row
-// products run through an expert's token blocks fastest, then its feature
-// tiles, so that CTAs running together share weight tiles and rows in L2.
+// The units of a CTA.  DW: every expert's tiles, feature tiles fastest.
 template <int MODE, int NB>
 struct Units {
     const Args& a;
-    const LiveExpert* tab;   // FWD, DX
+    RowUnits<NB> rows;
     const int* off;          // DW: offsets in shared memory
-    int live, mt;
     long long u, total;
 
-    __device__ Units(const Args& a_, const LiveExpert* t, const int* o, int live_)
-        : a(a_), tab(t), off(o), live(live_), mt((a_.M + 127) / 128), u(blockIdx.x)
+    __device__ Units(const Args& a_, const LiveExpert* t, const int* o, int live)
+        : a(a_), rows(t, live, a_.M), off(o), u(blockIdx.x),
+          total((long long)a_.E * ((a_.M + 127) / 128) * ((a_.N + NB - 1) / NB))
     {
-        if (MODE == DW)
-            total = (long long)a.E * mt * ((a.N + NB - 1) / NB);
-        else
-            total = live ? (long long)tab[live].pre * mt : 0;
     }
     __device__ bool next(Unit& v)
     {
-        if (u >= total) return false;
         if (MODE == DW) {
-            const int nt = (a.N + NB - 1) / NB, per = mt * nt;
+            if (u >= total) return false;
+            const int mt = (a.M + 127) / 128, per = mt * ((a.N + NB - 1) / NB);
             const int e = (int)(u / per), r = (int)(u % per);
             int lo = off[e], hi = off[e + 1];
             if (lo < 0 || hi < lo || hi > a.rows) lo = hi = 0;
@@ -97,20 +89,12 @@ struct Units {
             v.k0 = lo;
             v.steps = (hi - lo + 63) / 64;
             v.tail = hi - lo - (v.steps - 1) * 64;
+            u += gridDim.x;
         } else {
-            const LiveExpert L = tab[find_live(tab, live, mt, u)];
-            const long long r = u - (long long)L.pre * mt;
-            const int nt = (L.r1 - L.r0 + NB - 1) / NB;
-            const int t = (int)(r % nt);
-            v.e = L.e;
-            v.m0 = (int)(r / nt) * 128;
-            v.c0 = L.r0 + t * NB;
-            v.n = min(NB, L.r1 - v.c0);
-            v.k0 = 0;
-            v.steps = (a.K + 63) / 64;
-            v.tail = 64;
+            RowUnit w;
+            if (!rows.next(w)) return false;
+            v = {w.e, w.m0, w.r0, w.n, 0, (a.K + 63) / 64, 64};
         }
-        u += gridDim.x;
         return true;
     }
 };
@@ -306,14 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-int device_sms(int* sms)
-{
-    int dev = 0;
-    MOE_CUDA_TRY(cudaGetDevice(&dev));
-    MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
-    return MOE_OK;
-}
-
 template <int MODE, int NB>
 int launch_nb(Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
 {
@@ -332,21 +308,6 @@ int launch_nb(Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_
     MOE_LAUNCH_CHECK();
     return MOE_OK;
 }
-
-// Checks common to the products; MOE_OK to go on.
-int check_sizes(int experts, int in, int out, int rows)
-{
-    if (experts <= 0 || in <= 0 || in % 8 || out <= 0 || out % 8 || rows < 0) return MOE_ERR_INVALID_ARG;
-    if (experts > kMaxExperts || in > kMaxDim || out > kMaxDim || rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
-}
-// A matrix of 16-byte aligned rows of `width` elements of `size` bytes.
-bool rows_ok(const void* p, int64_t ld, int64_t width, int size)
-{
-    return p && !((uintptr_t)p & 15) && ld >= width && ld < ((int64_t)1 << 36) && (ld * size) % 16 == 0;
-}
-bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_BF16; }
-int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
 
 bool map_rows(CUtensorMap* m, const void* p, int64_t ld, int width, int rows, int box)
 {
@@ -428,7 +389,7 @@ extern "C" int moe_grouped_gemm(int32_t experts, int32_t in, int32_t out, const 
                                 const uint16_t* d_w, const int32_t* d_offsets, int32_t rows, void* d_y, int64_t ldy,
                                 int32_t y_dtype, void* stream)
 {
-    if (int rc = check_sizes(experts, in, out, rows)) return rc;
+    if (int rc = check_gemm_sizes(experts, in, out, rows, 8)) return rc;
     if (!out_dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!d_offsets || !rows_ok(d_x, ldx, in, 2) || !rows_ok(d_w, in, in, 2) || !rows_ok(d_y, ldy, out, dtype_size(y_dtype)))
@@ -440,7 +401,7 @@ extern "C" int moe_grouped_gemm_dx(int32_t experts, int32_t in, int32_t out, con
                                    const uint16_t* d_w, const int32_t* d_offsets, int32_t rows, void* d_dx,
                                    int64_t lddx, int32_t dx_dtype, void* stream)
 {
-    if (int rc = check_sizes(experts, in, out, rows)) return rc;
+    if (int rc = check_gemm_sizes(experts, in, out, rows, 8)) return rc;
     if (!out_dtype_ok(dx_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!d_offsets || !rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_w, in, in, 2) ||
@@ -453,7 +414,7 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
                                    const uint16_t* d_x, int64_t ldx, const int32_t* d_offsets, int32_t rows,
                                    void* d_dw, int32_t dw_dtype, int32_t accumulate, void* stream)
 {
-    if (int rc = check_sizes(experts, in, out, rows)) return rc;
+    if (int rc = check_gemm_sizes(experts, in, out, rows, 8)) return rc;
     if (!out_dtype_ok(dw_dtype) || !d_offsets || !rows_ok(d_dw, in, in, dtype_size(dw_dtype))) return MOE_ERR_INVALID_ARG;
     if (rows > 0 && (!rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_x, ldx, in, 2))) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = as_stream(stream);

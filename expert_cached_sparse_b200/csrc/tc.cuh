@@ -232,16 +232,70 @@ __device__ __forceinline__ int build_live(const int32_t* __restrict__ offsets, i
     return live;
 }
 
-// Index of the live expert that unit u (mt feature tiles per token block) belongs to.
-__device__ __forceinline__ int find_live(const LiveExpert* tab, int live, int mt, long long u)
-{
-    int lo = 0, hi = live - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((long long)tab[mid].pre * mt <= u) lo = mid;
-        else hi = mid - 1;
+// A tile of the row products: 128 features from m0 on, n rows from r0 on, of
+// expert e's matrix.
+struct RowUnit {
+    int e, m0, r0, n;
+};
+
+// The tiles of a CTA: u = blockIdx.x, blockIdx.x + gridDim.x, ... .  An
+// expert's token blocks run fastest, then its feature tiles, so that CTAs
+// running together share weight tiles and rows in L2.
+template <int NB>
+struct RowUnits {
+    const LiveExpert* tab;
+    int live, mt;
+    long long u, total;
+
+    __device__ RowUnits(const LiveExpert* t, int live_, int M)
+        : tab(t), live(live_), mt((M + 127) / 128), u(blockIdx.x), total((long long)t[live_].pre * mt)
+    {
     }
-    return lo;
+    __device__ bool next(RowUnit& v)
+    {
+        if (u >= total) return false;
+        int lo = 0, hi = live - 1;   // the last live expert whose first tile is at most u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((long long)tab[mid].pre * mt <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        const LiveExpert L = tab[lo];
+        const long long r = u - (long long)L.pre * mt;
+        const int nt = (L.r1 - L.r0 + NB - 1) / NB;
+        v.e = L.e;
+        v.m0 = (int)(r / nt) * 128;
+        v.r0 = L.r0 + (int)(r % nt) * NB;
+        v.n = min(NB, L.r1 - v.r0);
+        u += gridDim.x;
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------ host: checks common to the products
+constexpr int64_t kMaxGemmDim = 1 << 20;
+constexpr int kSmemMax = 227 * 1024;
+
+static inline int check_gemm_sizes(int experts, int in, int out, int rows, int in_multiple)
+{
+    if (experts <= 0 || in <= 0 || in % in_multiple || out <= 0 || out % 8 || rows < 0) return MOE_ERR_INVALID_ARG;
+    if (experts > kMaxExperts || in > kMaxGemmDim || out > kMaxGemmDim || rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+// A matrix of 16-byte aligned rows of `width` elements of `size` bytes.
+static inline bool rows_ok(const void* p, int64_t ld, int64_t width, int size)
+{
+    return p && !((uintptr_t)p & 15) && ld >= width && ld < ((int64_t)1 << 36) && (ld * size) % 16 == 0;
+}
+static inline bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_BF16; }
+static inline int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
+
+static inline int device_sms(int* sms)
+{
+    int dev = 0;
+    MOE_CUDA_TRY(cudaGetDevice(&dev));
+    MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+    return MOE_OK;
 }
 
 }  // namespace moe

@@ -15,24 +15,45 @@ constexpr int64_t kMaxDim = 1 << 20;
 
 __device__ __forceinline__ float block_scale(float m) { return m < kTinyBlock ? 1.0f : __fdiv_rn(m, kE4m3Max); }
 
-// Eight consecutive elements, widened to fp32.
+// Eight consecutive elements as they lie in memory; bf16 ones stay packed
+// (four registers instead of eight while loads are in flight).
 template <bool XF32>
-__device__ __forceinline__ void load8(const void* p, float (&v)[8])
-{
-    if (XF32) {
-        const float4 a = __ldg(static_cast<const float4*>(p)), b = __ldg(static_cast<const float4*>(p) + 1);
+struct Run8;
+
+template <>
+struct Run8<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* p)
+    {
+        a = __ldg(static_cast<const float4*>(p));
+        b = __ldg(static_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void forget() {}
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 u = __ldg(static_cast<const uint4*>(p));
+    }
+};
+
+template <>
+struct Run8<false> {
+    uint4 u;
+    __device__ __forceinline__ void load(const void* p) { u = __ldg(static_cast<const uint4*>(p)); }
+    // keeps the compiler from holding the widened values instead of the packed ones
+    __device__ __forceinline__ void forget() { asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-            v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
-}
+};
 
 __device__ __forceinline__ float max8(const float (&v)[8])
 {
@@ -42,93 +63,137 @@ __device__ __forceinline__ float max8(const float (&v)[8])
     return m;
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s)
+// silu(g) * u: expf within 2 units in the last place, the quotient too.
+__device__ __forceinline__ float swiglu1(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+
+// The block's divisor: v / s for its 128 or 16384 elements by Markstein's
+// method (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with y the correctly
+// rounded 1 / s, q0 = v y and the exact residual r = v - q0 s, q0 + r y rounds
+// to the correctly rounded v / s: three instructions an element against about
+// forty of a division.  An infinite s gives y = 0 and takes the part of a zero
+// in the residual, so that finite / inf is 0 and inf / inf NaN.  Quotients
+// whose residual underflows are below 2^-16: code 0 either way.
+struct Divisor {
+    float s, y;
+    __device__ __forceinline__ explicit Divisor(float scale)
+    {
+        s = isinf(scale) ? 0.0f : scale;
+        y = isinf(scale) ? 0.0f : __fdiv_rn(1.0f, scale);
+    }
+    __device__ __forceinline__ float operator()(float v) const
+    {
+        const float q = __fmul_rn(v, y);
+        return __fmaf_rn(__fmaf_rn(-q, s, v), y, q);
+    }
+};
+
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const Divisor& d)
 {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float2 r = make_float2(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
+        const float2 r = make_float2(d(v[2 * i]), d(v[2 * i + 1]));
         w[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
     }
     return make_uint2(w[0], w[1]);
 }
 
-// 16 lanes per 1 x 128 block, eight columns each; consecutive half-warps take
-// consecutive rows of one block column, so that their scales are adjacent.
-template <bool XF32, bool SWIGLU>
+// A CTA takes 16 rows by BPT block columns at a time: half a warp per row
+// (eight columns a lane), all BPT loads in flight before the first block is
+// worked on.  The 16 rows' scales of a block column are adjacent.
+template <bool XF32, bool SWIGLU, int BPT>
 __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ldx, int rows, int cols,
                                                         uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
 {
-    const int kb = (cols + 127) / 128, sub = threadIdx.x & 15;
-    const int64_t total = (int64_t)((rows + 15) / 16) * 16 * kb;   // rows of whole 16-row groups, so warps stay whole
-    const int64_t step = (int64_t)gridDim.x * 16;
-    for (int64_t i = blockIdx.x * (int64_t)16 + (threadIdx.x >> 4); i < total; i += step) {
-        const int64_t g = i / (16 * kb);
-        const int r = (int)(g * 16 + (i & 15)), b = (int)((i >> 4) % kb), c = b * 128 + sub * 8;
-        const bool live = r < rows && c < cols;
-        float v[8];
+    constexpr int SZ = XF32 ? 4 : 2;
+    const int kb = (cols + 127) / 128, per = (kb + BPT - 1) / BPT, sub = threadIdx.x & 15;
+    const int total = (rows + 15) / 16 * per;
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+        const int r = i / per * 16 + (threadIdx.x >> 4), b0 = i % per * BPT;
+        const char* p = static_cast<const char*>(x) + (int64_t)r * ldx * SZ;
+        Run8<XF32> x8[BPT], u8[SWIGLU ? BPT : 1];
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = 0.0f;
-        if (live) {
-            const int64_t at = (int64_t)r * ldx + c;
-            const char* p = static_cast<const char*>(x);
-            const int sz = XF32 ? 4 : 2;
-            load8<XF32>(p + at * sz, v);
-            if (SWIGLU) {
-                float u[8];
-                load8<XF32>(p + (at + cols) * sz, u);
-#pragma unroll
-                for (int j = 0; j < 8; j++) v[j] = v[j] / (1.0f + expf(-v[j])) * u[j];
+        for (int j = 0; j < BPT; j++) {
+            const int c = (b0 + j) * 128 + sub * 8;
+            if (r < rows && c < cols) {
+                x8[j].load(p + (int64_t)c * SZ);
+                if (SWIGLU) u8[j].load(p + ((int64_t)cols + c) * SZ);
+            } else {
+                x8[j].zero();
+                if (SWIGLU) u8[j].zero();
             }
         }
-        float m = max8(v);
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float sc = block_scale(m);
-        if (live) {
-            *reinterpret_cast<uint2*>(q + (int64_t)r * ldq + c) = codes8(v, sc);
-            if (sub == 0) s[(int64_t)b * rows + r] = sc;
+        for (int j = 0; j < BPT; j++) {
+            const int b = b0 + j, c = b * 128 + sub * 8;
+            float v[8];
+            x8[j].get(v);
+            if (SWIGLU) {
+                float u[8];
+                u8[j].get(u);
+#pragma unroll
+                for (int k = 0; k < 8; k++) v[k] = swiglu1(v[k], u[k]);
+            }
+            float m = max8(v);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float sc = block_scale(m);
+            if (r < rows && c < cols) {
+                *reinterpret_cast<uint2*>(q + (int64_t)r * ldq + c) = codes8(v, Divisor(sc));
+                if (sub == 0) s[(int64_t)b * rows + r] = sc;
+            }
         }
     }
 }
 
-// One CTA per 128 x 128 block; each thread holds eight runs of eight columns.
+// One CTA per 128 x 128 block; each thread holds eight runs of eight columns
+// between the maximum and the codes, so the block is read once.
 template <bool XF32>
-__global__ void __launch_bounds__(256) quant_weight_kernel(const void* __restrict__ w, int64_t blocks, int out, int in,
-                                                           uint8_t* __restrict__ q, float* __restrict__ s)
+__global__ void __launch_bounds__(256, XF32 ? 2 : 4)
+    quant_weight_kernel(const void* __restrict__ w, int blocks, int out, int in, uint8_t* __restrict__ q,
+                        float* __restrict__ s)
 {
-    __shared__ float s_m[8];
+    __shared__ float s_m[2][8];
     const int nb = (out + 127) / 128, kb = (in + 127) / 128;
     const int tr = threadIdx.x >> 4, c8 = (threadIdx.x & 15) * 8;
-    for (int64_t i = blockIdx.x; i < blocks; i += gridDim.x) {
-        const int b = (int)(i % kb);
-        const int64_t en = i / kb;
+    int flip = 0;
+    for (int i = blockIdx.x; i < blocks; i += gridDim.x, flip ^= 1) {
+        const int en = i / kb, b = i - en * kb;
         const int64_t e = en / nb;
-        const int r0 = (int)(en % nb) * 128 + tr, c = b * 128 + c8;
-        float v[8][8];
-        float m = 0.0f;
+        const int r0 = en % nb * 128 + tr, c = b * 128 + c8;
+        Run8<XF32> w8[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int r = r0 + 16 * j;
+            if (r < out && c < in)
+                w8[j].load(static_cast<const char*>(w) + ((e * out + r) * in + c) * (XF32 ? 4 : 2));
+            else
+                w8[j].zero();
+        }
+        float v[8], m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            w8[j].get(v);
+            m = fmaxf(m, max8(v));
+            w8[j].forget();
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((threadIdx.x & 31) == 0) s_m[flip][threadIdx.x >> 5] = m;   // two sets: one barrier a block
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; j++) m = fmaxf(m, s_m[flip][j]);
+        const float sc = block_scale(m);
+        const Divisor div(sc);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int r = r0 + 16 * j;
             if (r < out && c < in) {
-                load8<XF32>(static_cast<const char*>(w) + ((e * out + r) * in + c) * (XF32 ? 4 : 2), v[j]);
-                m = fmaxf(m, max8(v[j]));
+                w8[j].get(v);
+                *reinterpret_cast<uint2*>(q + (e * out + r) * in + c) = codes8(v, div);
             }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; j++) m = fmaxf(m, s_m[j]);
-        const float sc = block_scale(m);
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int r = r0 + 16 * j;
-            if (r < out && c < in) *reinterpret_cast<uint2*>(q + (e * out + r) * in + c) = codes8(v[j], sc);
-        }
         if (threadIdx.x == 0) s[i] = sc;
-        __syncthreads();
     }
 }
 
@@ -159,12 +224,18 @@ extern "C" int moe_fp8_quantize_act(const void* d_x, int32_t x_dtype, int64_t ld
     cudaStream_t st = as_stream(stream);
     ProfScope ps(MOE_PROF_QUANT, st);
     prof_count(MOE_PROF_QUANT, 1);
-    const int64_t want = (int64_t)((rows + 15) / 16) * ((cols + 127) / 128);
-    const int cap = sm_count() * 8;
-    const int grid = (int)(want < cap ? want : cap);
+    // four blocks a thread once that still gives every SM several CTAs
+    const int64_t groups = (rows + 15) / 16, kb = (cols + 127) / 128;
+    const int sms = sm_count();
+    const bool wide = groups * ((kb + 3) / 4) >= 4 * sms;
+    const int64_t want = groups * (wide ? (kb + 3) / 4 : kb);
+    if (want > 0x7fffffff - 8 * sms) return MOE_ERR_UNSUPPORTED;
+    const int grid = (int)(want < 8 * sms ? want : 8 * sms);
     const bool f32 = x_dtype == MOE_DT_F32;
-    auto* kern = f32 ? (swiglu ? quant_act_kernel<true, true> : quant_act_kernel<true, false>)
-                     : (swiglu ? quant_act_kernel<false, true> : quant_act_kernel<false, false>);
+    auto* kern = wide ? (f32 ? (swiglu ? quant_act_kernel<true, true, 4> : quant_act_kernel<true, false, 4>)
+                             : (swiglu ? quant_act_kernel<false, true, 4> : quant_act_kernel<false, false, 4>))
+                      : (f32 ? (swiglu ? quant_act_kernel<true, true, 1> : quant_act_kernel<true, false, 1>)
+                             : (swiglu ? quant_act_kernel<false, true, 1> : quant_act_kernel<false, false, 1>));
     kern<<<grid, 256, 0, st>>>(d_x, ldx, rows, cols, d_q, ldq, d_s);
     MOE_LAUNCH_CHECK();
     return MOE_OK;
@@ -182,10 +253,11 @@ extern "C" int moe_fp8_quantize_weight(const void* d_w, int32_t w_dtype, int32_t
     ProfScope ps(MOE_PROF_QUANT, st);
     prof_count(MOE_PROF_QUANT, 1);
     const int64_t blocks = (int64_t)experts * ((out + 127) / 128) * ((in + 127) / 128);
-    const int cap = sm_count() * 8;
+    if (blocks > 0x7fffffff - 4096) return MOE_ERR_UNSUPPORTED;   // 35 TB of bf16
+    const int cap = sm_count() * (w_dtype == MOE_DT_F32 ? 2 : 4);
     const int grid = (int)(blocks < cap ? blocks : cap);
     auto* kern = w_dtype == MOE_DT_F32 ? quant_weight_kernel<true> : quant_weight_kernel<false>;
-    kern<<<grid, 256, 0, st>>>(d_w, blocks, out, in, d_q, d_s);
+    kern<<<grid, 256, 0, st>>>(d_w, (int)blocks, out, in, d_q, d_s);
     MOE_LAUNCH_CHECK();
     return MOE_OK;
 }

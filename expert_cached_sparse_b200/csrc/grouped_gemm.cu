@@ -5,8 +5,8 @@
 //   DW   dW_e[o][i] = sum_r dy[r][o] x[r][i]   over e's rows
 //
 // One kernel, three operand layouts.  A tile is 128 features (the tensor
-// core's M, one tensor-memory lane each: `out` for FWD, `in` for DX and DW) by
-// up to NB columns (N: rows for FWD and DX, `out` for DW), and the inner index
+// core's M, one tensor-memory lane each: `out` for FWD and DW, `in` for DX) by
+// up to NB columns (N: rows for FWD and DX, `in` for DW), and the inner index
 // advances 64 per pipeline stage.  The features are the operand that is never
 // ragged, so M is always full and N takes any multiple of 16: an expert with
 // one row costs a 128 x 16 tile, not a 128 x 128 one.  TMA brings each operand
@@ -47,7 +47,7 @@ struct Args {
     int64_t ldo;
     int out_f32, accumulate;
     int E, rows;
-    int M, N;        // features; DW: columns (`out`)
+    int M, N;        // features; DW: columns (`in`)
     int K;           // inner size (DW: ragged)
     int stages;
     int box;         // rows per copy of the ragged operand (FWD, DX)
@@ -56,7 +56,7 @@ struct Args {
 };
 
 struct Unit {
-    int e, m0, c0, n;   // expert, first feature, first column (row of the matrix, or `out` index), columns
+    int e, m0, c0, n;   // expert, first feature, first column (row of the matrix, or `in` index), columns
     int k0, steps;      // DW: first row; steps of 64
     int tail;           // DW: valid rows of the last step
 };
@@ -98,6 +98,86 @@ struct Units {
         return true;
     }
 };
+
+__device__ __forceinline__ void put(float* p, uint32_t d) { *p = __uint_as_float(d); }
+__device__ __forceinline__ void put(uint16_t* p, uint32_t d) { *p = f32_to_bf16_bits(__uint_as_float(d)); }
+
+// A warp's 32 features of n columns, ldo elements apart: each store is 32
+// adjacent elements of one column.  `mine`: whether the lane's feature exists.
+template <class T>
+__device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int n, bool mine)
+{
+    uint32_t d[16];
+    int c = 0;
+    for (; c + 16 <= n; c += 16) {
+        tmem_ld16(src + c, d);
+        wait_ld();
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                put(p, d[j]);
+                p += ldo;
+            }
+        }
+        __syncwarp();   // the warp's next tensor-memory load is a converged one
+    }
+    if (c < n) {
+        tmem_ld16(src + c, d);
+        wait_ld();
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < 16; j++)
+                if (c + j < n) put(p + j * ldo, d[j]);
+        }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+}
+
+// 8 (n < 16) or 16 adjacent elements of dW from index `at` on.
+__device__ __forceinline__ void store_row16(const Args& a, int64_t at, uint32_t (&d)[16], int n)
+{
+    const int half = n < 16 ? 1 : 2;   // `in` is a multiple of 8
+    if (a.out_f32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (j >= 2 * half) break;
+            float4 x = make_float4(__uint_as_float(d[4 * j]), __uint_as_float(d[4 * j + 1]),
+                                   __uint_as_float(d[4 * j + 2]), __uint_as_float(d[4 * j + 3]));
+            if (a.accumulate) {
+                const float4 b = o[j];
+                x = make_float4(x.x + b.x, x.y + b.y, x.z + b.z, x.w + b.w);
+            }
+            o[j] = x;
+        }
+    } else {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            if (j >= half) break;
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (a.accumulate) {
+                const uint4 b = o[j];
+                w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                float lo = __uint_as_float(d[8 * j + 2 * k]), hi = __uint_as_float(d[8 * j + 2 * k + 1]);
+                if (a.accumulate) {
+                    lo += bf16_bits_to_f32(w[k] & 0xFFFFu);
+                    hi += bf16_bits_to_f32(w[k] >> 16);
+                }
+                w[k] = pack_bf16(lo, hi);
+            }
+            o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
 
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -207,11 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (MODE == DW && s == v.steps - 1 && v.tail < 64) {
                     // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
                     kk = (v.tail + 15) / 16;
-                    const int z = 16 * kk - v.tail, chunks = 2 + (v.n + 63) / 64;
-                    for (int i = lane; i < z * 8 * chunks; i += 32) {
-                        const int c = i / (z * 8), r = i % (z * 8);
-                        *reinterpret_cast<uint4*>(sp + 8192 * c + 128 * v.tail + 16 * r) = make_uint4(0, 0, 0, 0);
-                    }
+                    const int z = 128 * (16 * kk - v.tail), chunks = 2 + (v.n + 63) / 64;
+                    for (int i = 16 * lane; i < z; i += 512)
+                        for (int c = 0; c < chunks; c++)
+                            *reinterpret_cast<uint4*>(sp + 8192 * c + 128 * v.tail + i) = make_uint4(0, 0, 0, 0);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
@@ -231,50 +310,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(smem_u32(&fin));   // every MMA completes before tensor memory is released
         mbar_drain(smem_u32(&fin), 0, err);
     } else {
-        // ============ epilogue: lane quarter q = warp % 4, one feature per thread.
-        // A warp's store is 32 consecutive features of one column.
+        // ============ epilogue: lane quarter q = warp % 4, one feature per thread
         const int q = warp & 3;
         int it = 0;
         bool ok = true;
         while (ok && units.next(v)) {
-            const int f = v.m0 + 32 * q + lane;
-            const int64_t at = (MODE == DW ? ((int64_t)v.e * a.N + v.c0) : (int64_t)v.c0) * a.ldo + f;
-            float* of = static_cast<float*>(a.out) + at;
-            uint16_t* oh = static_cast<uint16_t*>(a.out) + at;
-            const bool mine = f < a.M;
-            if (MODE == DW && v.steps == 0) {
-                if (mine && !a.accumulate)
-                    for (int c = 0; c < v.n; c++) {
-                        if (a.out_f32) of[c * a.ldo] = 0.0f;
-                        else oh[c * a.ldo] = 0;
-                    }
-                __syncwarp();
-                continue;
+            const int f = v.m0 + 32 * q + lane, ab = it & 1;
+            const bool none = MODE == DW && v.steps == 0;   // an expert without rows: its gradient is zero
+            if (none && a.accumulate) continue;
+            if (!none) {
+                if (!(ok = mbar_wait(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+                fence_after();
             }
-            const int ab = it & 1;
-            if (!(ok = mbar_wait(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
-            fence_after();
             const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
-            for (int c0 = 0; c0 < v.n; c0 += 16) {
-                uint32_t d[16];
-                tmem_ld16(src + c0, d);
-                wait_ld();
-                if (mine) {
+            const bool mine = f < a.M;
+            if (MODE == DW) {
+                // a thread's feature is a row of dW: 16 adjacent columns at a time
+                const int64_t at = ((int64_t)v.e * a.M + f) * a.N + v.c0;
+                for (int c = 0; c < v.n; c += 16) {
+                    uint32_t d[16];
+                    if (none) {
 #pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        if (c0 + j >= v.n) break;
-                        float x = __uint_as_float(d[j]);
-                        const int64_t o = (int64_t)(c0 + j) * a.ldo;
-                        if (a.out_f32) {
-                            if (MODE == DW && a.accumulate) x += of[o];
-                            of[o] = x;
-                        } else {
-                            if (MODE == DW && a.accumulate) x += bf16_bits_to_f32(oh[o]);
-                            oh[o] = f32_to_bf16_bits(x);
-                        }
+                        for (int j = 0; j < 16; j++) d[j] = 0;
+                    } else {
+                        tmem_ld16(src + c, d);
+                        wait_ld();
                     }
+                    if (mine) store_row16(a, at + c, d, v.n - c);
+                    __syncwarp();   // the warp's next tensor-memory load is a converged one
                 }
-                __syncwarp();   // the warp's next tensor-memory load is a converged one
+                if (none) continue;
+            } else if (a.out_f32) {
+                store_cols(static_cast<float*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
+            } else {
+                store_cols(static_cast<uint16_t*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
             }
             fence_before();
             __syncwarp();
@@ -431,11 +500,11 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     a.accumulate = accumulate ? 1 : 0;
     a.E = experts;
     a.rows = rows;
-    a.M = in;
-    a.N = out;
+    a.M = out;
+    a.N = in;
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
     CUtensorMap ta, tb;
-    if (!map_rows(&ta, d_x, ldx, in, rows, 64) || !map_rows(&tb, d_dy, lddy, out, rows, 64)) return MOE_ERR_CUDA;
+    if (!map_rows(&ta, d_dy, lddy, out, rows, 64) || !map_rows(&tb, d_x, ldx, in, rows, 64)) return MOE_ERR_CUDA;
     return launch_nb<DW, 256>(a, ta, tb, st);
 }

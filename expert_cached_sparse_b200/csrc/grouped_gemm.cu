@@ -20,11 +20,11 @@
 // inner index, so a last step's surplus rows are zeroed in shared memory, in
 // both operands (a NaN there must not meet a zero), before the MMAs read them.
 //
-// One persistent CTA per SM: warp 0 copies, warp 1 issues the MMAs into one
-// of two accumulators, warps 2-5 read the other one back and store it.  Every
-// wait is bounded; a timeout records MOE_ERR_TIMEOUT, raises the CTA's abort
-// flag so that the other roles stop, and the CTA waits for its own copies and
-// MMAs before it returns.
+// One persistent CTA per SM: warps 0 and 2 copy the two operands, warp 1
+// issues the MMAs into one of two accumulators, warps 4-7 read the other one
+// back and store it.  Every wait is bounded; a timeout records
+// MOE_ERR_TIMEOUT, raises the CTA's abort flag so that the other roles stop,
+// and the CTA waits for its own copies and MMAs before it returns.
 #include "tc.cuh"
 
 namespace moe {
@@ -35,9 +35,10 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
+constexpr int kStaging = 4 * 2 * 4096;
 
 enum Mode { FWD, DX, DW };
 
@@ -46,11 +47,13 @@ struct Args {
     void* out;
     int64_t ldo;
     int out_f32, accumulate;
+    int direct;      // DW: sums added to bf16 ones in registers
     int E, rows;
     int M, N;        // features; DW: columns (`in`)
     int K;           // inner size (DW: ragged)
     int stages;
-    int box;         // rows per copy of the ragged operand (FWD, DX)
+    int box;         // smallest height of a copy of the ragged operand (FWD, DX)
+    int chunks_a, chunks_b;   // whether one copy brings all 64-column chunks of an MN-major operand
     long long wait;  // limit of every bounded wait, in SM clock cycles
     int withhold;    // testing: CTA 0 leaves its first stage unfilled
 };
@@ -135,62 +138,46 @@ __device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int 
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
-    return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi)
+{
+    return pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
 }
 
-// 8 (n < 16) or 16 adjacent elements of dW from index `at` on.
-__device__ __forceinline__ void store_row16(const Args& a, int64_t at, uint32_t (&d)[16], int n)
+// Adds 8 (n < 16) or 16 adjacent elements to bf16 ones: fp32 sums, one rounding.
+__device__ __forceinline__ void add_row16(uint16_t* p, const uint32_t (&d)[16], int n)
 {
-    const int half = n < 16 ? 1 : 2;   // `in` is a multiple of 8
-    if (a.out_f32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+    uint4* o = reinterpret_cast<uint4*>(p);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (j >= 2 * half) break;
-            float4 x = make_float4(__uint_as_float(d[4 * j]), __uint_as_float(d[4 * j + 1]),
-                                   __uint_as_float(d[4 * j + 2]), __uint_as_float(d[4 * j + 3]));
-            if (a.accumulate) {
-                const float4 b = o[j];
-                x = make_float4(x.x + b.x, x.y + b.y, x.z + b.z, x.w + b.w);
-            }
-            o[j] = x;
-        }
-    } else {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+    for (int j = 0; j < 2; j++) {
+        if (j && n < 16) break;   // `in` is a multiple of 8
+        const uint4 b = o[j];
+        uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            if (j >= half) break;
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (a.accumulate) {
-                const uint4 b = o[j];
-                w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                float lo = __uint_as_float(d[8 * j + 2 * k]), hi = __uint_as_float(d[8 * j + 2 * k + 1]);
-                if (a.accumulate) {
-                    lo += bf16_bits_to_f32(w[k] & 0xFFFFu);
-                    hi += bf16_bits_to_f32(w[k] >> 16);
-                }
-                w[k] = pack_bf16(lo, hi);
-            }
-            o[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int k = 0; k < 4; k++)
+            w[k] = pack_bf16(__uint_as_float(d[8 * j + 2 * k]) + bf16_bits_to_f32(w[k] & 0xFFFFu),
+                             __uint_as_float(d[8 * j + 2 * k + 1]) + bf16_bits_to_f32(w[k] >> 16));
+        o[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
-    gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a)
+    gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
+              const __grid_constant__ CUtensorMap tm_out, const Args a)
 {
     constexpr int STAGE = kABytes + NB * 128;
     constexpr uint32_t TMEM = 2 * NB < 32 ? 32 : 2 * NB;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
     __shared__ uint32_t s_tmem;
+    __shared__ volatile long long s_issued[2];
     __shared__ int s_abort, s_scan[2 * kThreads / 32];
     unsigned char* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    LiveExpert* tab = reinterpret_cast<LiveExpert*>(ring + (size_t)a.stages * STAGE);
+    unsigned char* staging = ring + (size_t)a.stages * STAGE;   // DW: 4 warps x 2 tiles of 32 rows x 128 bytes
+    LiveExpert* tab = reinterpret_cast<LiveExpert*>(staging + (MODE == DW ? kStaging : 0));
     int* off = reinterpret_cast<int*>(tab);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort_v = &s_abort;
@@ -199,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < a.stages; i++) {
-            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&full[i]), 2);   // both copy warps
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -211,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) {
         tma_prefetch(&tm_a);
-        tma_prefetch(&tm_b);
+    } else if (warp == 2) {
+        for (int i = 0; i < kRowMaps && a.box << i <= NB; i++) tma_prefetch(&tm_b.m[i]);
     }
     if (warp == 1) tmem_alloc(smem_u32(&s_tmem), TMEM);
     fence_before();
@@ -227,45 +215,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     Units<MODE, NB> units(a, tab, off, live);
     Unit v;
 
-    if (warp == 0) {
-        // ============ copies (the whole warp walks the loop, one elected lane issues)
+    if (warp == 0 || warp == 2) {
+        // ============ copies: warp 0 the features (A), warp 2 the columns (B);
+        // the whole warp walks the loop, one elected lane issues
+        const bool is_a = warp == 0;
         int st = 0, withheld = -1;
         uint32_t ph = 0;
         long long issued = 0;
         bool ok = true;
         while (ok && units.next(v)) {
-            const int nbox = MODE == DW ? (v.n + 63) / 64 : (v.n + a.box - 1) / a.box;
-            const uint32_t bytes = kABytes + (uint32_t)(MODE == DW ? nbox * 8192 : nbox * a.box * 128);
+            const int ub = MODE == DW ? (a.chunks_b ? NB / 64 : (v.n + 63) / 64) : row_units(v.n, a.box);
+            const uint32_t bytes = is_a ? kABytes : (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
             for (int s = 0; s < v.steps; s++) {
                 if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
                 const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
+                const int k = v.k0 + 64 * s;
                 if (a.withhold && blockIdx.x == 0 && issued == 0) {
                     withheld = st;   // testing: never filled, so the wait for it runs out
-                } else {
+                } else if (is_a) {
                     mbar_expect_tx(bar, bytes);
-                    const int k = v.k0 + 64 * s;
                     if (MODE == FWD) {
                         tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
                     } else if (MODE == DX) {
-                        tma_3d(sa, &tm_a, v.m0, k, v.e, bar);
-                        tma_3d(sa + 8192, &tm_a, v.m0 + 64, k, v.e, bar);
+                        if (a.chunks_a) {
+                            tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
+                        } else {
+                            tma_3d(sa, &tm_a, v.m0, k, v.e, bar);
+                            tma_3d(sa + 8192, &tm_a, v.m0 + 64, k, v.e, bar);
+                        }
+                    } else if (a.chunks_a) {
+                        tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
                     } else {
                         tma_2d(sa, &tm_a, v.m0, k, bar);
                         tma_2d(sa + 8192, &tm_a, v.m0 + 64, k, bar);
                     }
-                    if (MODE == DW)
-                        for (int i = 0; i < nbox; i++) tma_2d(sb + 8192 * i, &tm_b, v.c0 + 64 * i, k, bar);
+                } else {
+                    mbar_expect_tx(bar, bytes);
+                    if (MODE != DW)
+                        tma_rows(sb, tm_b, k, v.c0, ub, a.box, bar);
+                    else if (a.chunks_b)
+                        tma_3d(sb, &tm_b.m[0], 0, k, v.c0 / 64, bar);
                     else
-                        for (int i = 0; i < nbox; i++) tma_2d(sb + 128 * a.box * i, &tm_b, k, v.c0 + a.box * i, bar);
+                        for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.c0 + 64 * i, k, bar);
                 }
                 issued++;
                 if (++st == a.stages) { st = 0; ph ^= 1; }
             }
         }
-        // every issued copy lands before the CTA exits (stage i was last
-        // filled in this pass over the ring if i < st, else in the previous one)
-        for (int i = 0; i < a.stages && i < issued; i++)
-            if (i != withheld) mbar_drain(smem_u32(&full[i]), i < st ? ph : (ph ^ 1), err);
+        // Every issued copy lands before the CTA exits.  After an abort one warp
+        // may be ahead: the other arrives for the stages it did not fill, so
+        // that their phases complete with the copies in flight.
+        if (lane == 0) s_issued[is_a] = issued;
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        const long long most = max(s_issued[0], s_issued[1]);
+        if (lane == 0)
+            for (long long i = issued; i < most; i++) mbar_arrive(smem_u32(&full[i % a.stages]));
+        if (is_a)
+            for (long long i = most > a.stages ? most - a.stages : 0; i < most; i++)
+                if ((int)(i % a.stages) != withheld)
+                    mbar_drain(smem_u32(&full[i % a.stages]), (uint32_t)(i / a.stages) & 1, err);
     } else if (warp == 1) {
         // ============ MMAs
         int st = 0, it = 0;
@@ -309,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(smem_u32(&fin));   // every MMA completes before tensor memory is released
         mbar_drain(smem_u32(&fin), 0, err);
-    } else {
+    } else if (warp >= 4) {
         // ============ epilogue: lane quarter q = warp % 4, one feature per thread
         const int q = warp & 3;
-        int it = 0;
+        int it = 0, turn = 0;
         bool ok = true;
         while (ok && units.next(v)) {
             const int f = v.m0 + 32 * q + lane, ab = it & 1;
@@ -324,21 +332,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
             const bool mine = f < a.M;
-            if (MODE == DW) {
+            if (MODE == DW && a.direct) {
                 // a thread's feature is a row of dW: 16 adjacent columns at a time
                 const int64_t at = ((int64_t)v.e * a.M + f) * a.N + v.c0;
                 for (int c = 0; c < v.n; c += 16) {
                     uint32_t d[16];
-                    if (none) {
-#pragma unroll
-                        for (int j = 0; j < 16; j++) d[j] = 0;
-                    } else {
-                        tmem_ld16(src + c, d);
-                        wait_ld();
-                    }
-                    if (mine) store_row16(a, at + c, d, v.n - c);
+                    tmem_ld16(src + c, d);
+                    wait_ld();
+                    if (mine) add_row16(static_cast<uint16_t*>(a.out) + at + c, d, v.n - c);
                     __syncwarp();   // the warp's next tensor-memory load is a converged one
                 }
+            } else if (MODE == DW) {
+                // a warp's 32 rows of dW go out by TMA, 128 bytes of each at a time, through
+                // two swizzled tiles in shared memory (zeros for an expert without rows)
+                const int w = a.out_f32 ? 32 : 64;
+                if (v.m0 + 32 * q < a.M)
+                    for (int c = 0; c < v.n; c += w, turn ^= 1) {
+                        unsigned char* tile = staging + 8192 * q + 4096 * turn;
+                        if (lane == 0) bulk_wait_read<1>();
+                        __syncwarp();
+                        for (int h = 0; h < w / 32; h++) {
+                            uint32_t d[32];
+                            if (none) {
+#pragma unroll
+                                for (int j = 0; j < 32; j++) d[j] = 0;
+                            } else {
+                                tmem_ld16(src + c + 32 * h, d);
+                                tmem_ld16(src + c + 32 * h + 16, d + 16);
+                                wait_ld();
+                            }
+                            unsigned char* row = tile + 128 * lane;
+                            if (a.out_f32) {
+#pragma unroll
+                                for (int j = 0; j < 8; j++)
+                                    *reinterpret_cast<uint4*>(row + 16 * (j ^ (lane & 7))) =
+                                        make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; j++)
+                                    *reinterpret_cast<uint4*>(row + 16 * ((j + 4 * h) ^ (lane & 7))) =
+                                        make_uint4(pack_bf16(d[8 * j], d[8 * j + 1]), pack_bf16(d[8 * j + 2], d[8 * j + 3]),
+                                                   pack_bf16(d[8 * j + 4], d[8 * j + 5]),
+                                                   pack_bf16(d[8 * j + 6], d[8 * j + 7]));
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (a.accumulate) tma_add_3d(&tm_out, smem_u32(tile), v.c0 + c, v.m0 + 32 * q, v.e);
+                            else tma_store_3d(&tm_out, smem_u32(tile), v.c0 + c, v.m0 + 32 * q, v.e);
+                            bulk_commit();
+                        }
+                    }
                 if (none) continue;
             } else if (a.out_f32) {
                 store_cols(static_cast<float*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
@@ -350,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
             it++;
         }
+        if (MODE == DW && lane == 0) bulk_wait();   // the staging tiles are read, the stores done
     }
     fence_before();
     __syncthreads();
@@ -360,29 +406,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int MODE, int NB>
-int launch_nb(Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
+int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NB * 128;
     int sms = 0;
     if (int rc = device_sms(&sms)) return rc;
     const int table = (int)align_up(MODE == DW ? sizeof(int) * (a.E + 1) : sizeof(LiveExpert) * (a.E + 1), 128);
-    a.stages = (kSmemMax - 2048 - table) / STAGE;   // 1 KB static, 1 KB alignment slack
+    const int fixed = 1024 + (MODE == DW ? kStaging : 0) + table;   // alignment slack, staging tiles, table
+    a.stages = (kSmemMax - 1024 - fixed) / STAGE;                    // 1 KB static
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    const int smem = 1024 + a.stages * STAGE + table;
+    const int smem = fixed + a.stages * STAGE;
     auto* kern = gg_kernel<MODE, NB>;
     MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    kern<<<sms, kThreads, smem, st>>>(ta, tb, a);
+    kern<<<sms, kThreads, smem, st>>>(ta, tb, to, a);
     MOE_LAUNCH_CHECK();
     return MOE_OK;
 }
 
-bool map_rows(CUtensorMap* m, const void* p, int64_t ld, int width, int rows, int box)
+// An MN-major operand [batch][K][width] (batch 0: no such dimension) in 64
+// inner rows by `chunks` 64-column chunks a copy.  Where the width is whole
+// chunks, they are a dimension of the map and one copy brings them all;
+// otherwise a copy brings one, and *whole is false.
+bool map_mn(CUtensorMap* m, int* whole, const void* p, int64_t ld, int width, int K, int chunks, int batch)
 {
-    const uint64_t dims[2] = {(uint64_t)width, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
-    const uint32_t b[2] = {64, (uint32_t)box};
-    return encode_map(m, false, 2, p, dims, strides, b);
+    *whole = width % 64 == 0;
+    if (*whole) {
+        const uint64_t dims[4] = {64, (uint64_t)K, (uint64_t)width / 64, (uint64_t)batch};
+        const uint64_t strides[3] = {(uint64_t)ld * 2, 128, (uint64_t)ld * K * 2};
+        const uint32_t box[4] = {64, 64, (uint32_t)chunks, 1};
+        return encode_map(m, E_BF16, batch ? 4 : 3, p, dims, strides, box);
+    }
+    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)K, (uint64_t)batch};
+    const uint64_t strides[2] = {(uint64_t)ld * 2, (uint64_t)ld * K * 2};
+    const uint32_t box[3] = {64, 64, 1};
+    return encode_map(m, E_BF16, batch ? 3 : 2, p, dims, strides, box);
 }
 
 // Products of rows with weights: y = x W^T (FWD) or dx = dy W (DX).
@@ -401,15 +460,21 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     a.K = MODE == FWD ? in : out;
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
-    CUtensorMap ta, tb;
-    const uint64_t dims[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)E};
-    const uint64_t strides[2] = {(uint64_t)in * 2, (uint64_t)in * out * 2};
-    const uint32_t box[3] = {64, MODE == FWD ? 128u : 64u, 1};
+    CUtensorMap ta;
+    RowMaps tb;
+    if (MODE == FWD) {
+        const uint64_t dims[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)E};
+        const uint64_t strides[2] = {(uint64_t)in * 2, (uint64_t)in * out * 2};
+        const uint32_t box[3] = {64, 128, 1};
+        if (!encode_map(&ta, E_BF16, 3, w, dims, strides, box)) return MOE_ERR_CUDA;
+    } else if (!map_mn(&ta, &a.chunks_a, w, in, in, out, 2, E)) {
+        return MOE_ERR_CUDA;
+    }
     const bool small = rows <= 16 * (int64_t)E;
-    a.box = small ? 16 : 64;
-    if (!encode_map(&ta, false, 3, w, dims, strides, box) || !map_rows(&tb, x, ldx, a.K, rows, a.box)) return MOE_ERR_CUDA;
+    a.box = small ? 16 : 32;
+    if (!encode_rows(&tb, E_BF16, x, ldx, a.K, rows, a.box, small ? 32 : 256)) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return small ? launch_nb<MODE, 32>(a, ta, tb, st) : launch_nb<MODE, 256>(a, ta, tb, st);
+    return small ? launch_nb<MODE, 32>(a, ta, tb, ta, st) : launch_nb<MODE, 256>(a, ta, tb, ta, st);
 }
 
 }  // namespace
@@ -427,7 +492,7 @@ int gemm_device_error(int clear)
 
 namespace tc {
 
-bool encode_map(CUtensorMap* m, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+bool encode_map(CUtensorMap* m, Elem type, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box)
 {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -442,11 +507,23 @@ bool encode_map(CUtensorMap* m, bool fp8, int rank, const void* base, const uint
         return reinterpret_cast<Encode>(f);
     }();
     if (!encode) return false;
-    const cuuint32_t ones[3] = {1, 1, 1};
-    return encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
-                  const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUtensorMapDataType t = type == E_U8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : type == E_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode(m, t, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_rows(RowMaps* r, Elem type, const void* p, int64_t ld, int width, int rows, int box, int most)
+{
+    const int size = type == E_U8 ? 1 : 2;
+    const uint64_t dims[2] = {(uint64_t)width, (uint64_t)rows}, strides[1] = {(uint64_t)ld * size};
+    for (int i = 0; i < kRowMaps && box << i <= most; i++) {
+        const uint32_t b[2] = {128u / size, (uint32_t)(box << i)};
+        if (!encode_map(&r->m[i], type, 2, p, dims, strides, b)) return false;
+    }
+    return true;
 }
 
 }  // namespace tc
@@ -504,7 +581,16 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     a.N = in;
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
-    CUtensorMap ta, tb;
-    if (!map_rows(&ta, d_dy, lddy, out, rows, 64) || !map_rows(&tb, d_x, ldx, in, rows, 64)) return MOE_ERR_CUDA;
-    return launch_nb<DW, 256>(a, ta, tb, st);
+    a.direct = a.accumulate && !a.out_f32;
+    CUtensorMap ta, to;
+    RowMaps tb;
+    const uint64_t dims[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)experts};
+    const int size = dtype_size(dw_dtype);
+    const uint64_t strides[2] = {(uint64_t)in * size, (uint64_t)in * out * size};
+    const uint32_t box[3] = {128u / size, 32, 1};
+    if (!map_mn(&ta, &a.chunks_a, d_dy, lddy, out, rows, 2, 0) || !map_mn(&tb.m[0], &a.chunks_b, d_x, ldx, in, rows, 4, 0) ||
+        !encode_map(&to, a.out_f32 ? E_F32 : E_BF16, 3, d_dw, dims, strides, box))
+        return MOE_ERR_CUDA;
+    a.box = 256;   // one map of the columns
+    return launch_nb<DW, 256>(a, ta, tb, to, st);
 }

@@ -45,14 +45,14 @@ struct Args {
     int E, rows;
     int M, blocks;     // features; 128-column blocks
     int stages;
-    int box;           // rows per copy of the row operand
+    int box;           // smallest height of a copy of the row operand
     long long wait;    // limit of every bounded wait, in SM clock cycles
     int withhold;      // testing: CTA 0 leaves its first stage unfilled
 };
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads, 1)
-    gg8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a)
+    gg8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b, const Args a)
 {
     constexpr int STAGE = kABytes + NB * 128;
     constexpr int CW = NB / 2;                    // columns of one epilogue warp
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) {
         tma_prefetch(&tm_a);
-        tma_prefetch(&tm_b);
+        for (int i = 0; i < kRowMaps && a.box << i <= NB; i++) tma_prefetch(&tm_b.m[i]);
     }
     if (warp == 1) tmem_alloc(smem_u32(&s_tmem), TMEM);
     fence_before();
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long issued = 0;
         bool ok = true;
         while (ok && units.next(v)) {
-            const int nbox = (v.n + a.box - 1) / a.box;
-            const uint32_t bytes = kABytes + (uint32_t)(nbox * a.box * 128);
+            const int ub = row_units(v.n, a.box);
+            const uint32_t bytes = kABytes + (uint32_t)(ub * a.box * 128);
             for (int b = 0; b < a.blocks; b++) {
                 if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
                 const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     mbar_expect_tx(bar, bytes);
                     tma_3d(sa, &tm_a, 128 * b, v.m0, v.e, bar);
-                    for (int i = 0; i < nbox; i++) tma_2d(sb + 128 * a.box * i, &tm_b, 128 * b, v.r0 + a.box * i, bar);
+                    tma_rows(sb, tm_b, 128 * b, v.r0, ub, a.box, bar);
                 }
                 issued++;
                 if (++st == a.stages) { st = 0; ph ^= 1; }
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int NB>
-int launch_nb(Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
+int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NB * 128;
     int sms = 0;
@@ -302,14 +302,15 @@ extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, co
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
     const bool small = rows <= 16 * (int64_t)experts;
-    a.box = small ? 16 : 64;
-    CUtensorMap ta, tb;
+    a.box = small ? 16 : 32;
+    CUtensorMap ta;
+    RowMaps tb;
     const uint64_t wd[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)experts};
     const uint64_t wst[2] = {(uint64_t)in, (uint64_t)in * out};
     const uint32_t wb[3] = {128, 128, 1};
-    const uint64_t xd[2] = {(uint64_t)in, (uint64_t)rows}, xst[1] = {(uint64_t)ldxq};
-    const uint32_t xb[2] = {128, (uint32_t)a.box};
-    if (!encode_map(&ta, true, 3, d_wq, wd, wst, wb) || !encode_map(&tb, true, 2, d_xq, xd, xst, xb)) return MOE_ERR_CUDA;
+    if (!encode_map(&ta, E_U8, 3, d_wq, wd, wst, wb) ||
+        !encode_rows(&tb, E_U8, d_xq, ldxq, in, rows, a.box, small ? 32 : 128))
+        return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
     return small ? launch_nb<32>(a, ta, tb, st) : launch_nb<128>(a, ta, tb, st);
 }

@@ -92,6 +92,32 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                 : "memory");
+}
+// Stores of a converged warp's own tiles: ordered by one lane's bulk groups,
+// so commit and wait run on lane 0, which issues.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x),
+                 "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>   // all but the newest N groups have read their source
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -164,12 +190,40 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v)
 }
 
 // ------------------------------------------------------------------ host: tensor maps
-// A row-major tensor of `rank` dimensions (dims[0] innermost), strides in
-// bytes of dims 1.., copied in boxes whose inner extent is 128 bytes and
-// stored in the 128-byte swizzle.  Reads outside the tensor give zeros.
-// False when the driver refuses it.
-bool encode_map(CUtensorMap* m, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+// A tensor of `rank` dimensions (dims[0] innermost), strides in bytes of dims
+// 1.., copied in boxes whose inner extent is 128 bytes and that lie in shared
+// memory in the 128-byte swizzle.  Reads outside the tensor give zeros,
+// writes there nothing.  False when the driver refuses it.
+enum Elem { E_BF16, E_F32, E_U8 };
+bool encode_map(CUtensorMap* m, Elem type, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
+
+// The copies that bring n rows (n <= 256) of a row matrix, 128 bytes of each,
+// into shared memory: one map per box height box << i, as few copies as two
+// heights allow (the surplus rows cost L2 reads, but a copy's issue costs
+// more: see grouped_gemm.cu).
+constexpr int kRowMaps = 4;
+struct RowMaps {
+    CUtensorMap m[kRowMaps];
+};
+__device__ __forceinline__ int row_units(int n, int box)   // in boxes of the smallest height
+{
+    int u = (n + box - 1) / box;
+    while (__popc(u) > 2) u += u & -u;
+    return u;
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const RowMaps& maps, int x, int row, int units, int box,
+                                         uint32_t bar)
+{
+    for (int i = kRowMaps - 1; i >= 0; i--)
+        if (units >> i & 1) {
+            tma_2d(dst, &maps.m[i], x, row, bar);
+            dst += (uint32_t)(128 * box << i);
+            row += box << i;
+        }
+}
+// Maps of a row matrix with heights box, 2 box, ... up to `most`.
+bool encode_rows(RowMaps* r, Elem type, const void* p, int64_t ld, int width, int rows, int box, int most);
 
 }  // namespace tc
 

@@ -20,11 +20,19 @@
 // inner index, so a last step's surplus rows are zeroed in shared memory, in
 // both operands (a NaN there must not meet a zero), before the MMAs read them.
 //
-// One persistent CTA per SM: warps 0 and 2 copy the two operands, warp 1
-// issues the MMAs into one of two accumulators, warps 4-7 read the other one
-// back and store it.  Every wait is bounded; a timeout records
-// MOE_ERR_TIMEOUT, raises the CTA's abort flag so that the other roles stop,
-// and the CTA waits for its own copies and MMAs before it returns.
+// Tiles of many columns run on pairs of CTAs (CG = 2, the two SMs of a
+// cluster): 256 features by NB columns, each CTA holding its own 128 features
+// and half of the columns, so a column's bytes cross from L2 once for 256
+// features instead of once for 128.
+//
+// Roles, one persistent CTA or pair per SM or two: warps 0 and 2 copy the two
+// operands, warp 1 (of the pair's first CTA) issues the MMAs into one of two
+// accumulators, warps 4-7 read the other one back and store it.  Warp 3 works
+// between copies and MMAs where that is needed: it zeroes the surplus rows
+// (DW) and tells the pair's first CTA that a stage is in place (CG = 2).
+// Every wait is bounded; a timeout records MOE_ERR_TIMEOUT, raises the CTA's
+// abort flag so that the other roles stop, and the CTA waits for its own
+// copies and MMAs before it returns.
 #include "tc.cuh"
 
 namespace moe {
@@ -59,45 +67,52 @@ struct Args {
 };
 
 struct Unit {
-    int e, m0, c0, n;   // expert, first feature, first column (row of the matrix, or `in` index), columns
+    int e, m0, c0, n;   // expert, this CTA's first feature, first column (row of the matrix, or `in` index), columns
+    int cb, nb, nh;     // this CTA's share of the columns: first one, how many exist, how many the MMA takes
     int k0, steps;      // DW: first row; steps of 64
     int tail;           // DW: valid rows of the last step
 };
 
-// The units of a CTA.  DW: every expert's tiles, feature tiles fastest.
-template <int MODE, int NB>
+// The units of a CTA or pair.  DW: every expert's tiles, feature tiles fastest.
+template <int MODE, int NB, int CG>
 struct Units {
     const Args& a;
-    RowUnits<NB> rows;
+    RowUnits<NB, CG> rows;
     const int* off;          // DW: offsets in shared memory
+    const int rank;
     long long u, total;
 
-    __device__ Units(const Args& a_, const LiveExpert* t, const int* o, int live)
-        : a(a_), rows(t, live, a_.M), off(o), u(blockIdx.x),
-          total((long long)a_.E * ((a_.M + 127) / 128) * ((a_.N + NB - 1) / NB))
+    __device__ Units(const Args& a_, const LiveExpert* t, const int* o, int live, int rank_)
+        : a(a_), rows(t, live, a_.M), off(o), rank(rank_), u(blockIdx.x / CG),
+          total((long long)a_.E * ((a_.M + 128 * CG - 1) / (128 * CG)) * ((a_.N + NB - 1) / NB))
     {
     }
     __device__ bool next(Unit& v)
     {
         if (MODE == DW) {
             if (u >= total) return false;
-            const int mt = (a.M + 127) / 128, per = mt * ((a.N + NB - 1) / NB);
+            const int mt = (a.M + 128 * CG - 1) / (128 * CG), per = mt * ((a.N + NB - 1) / NB);
             const int e = (int)(u / per), r = (int)(u % per);
             int lo = off[e], hi = off[e + 1];
             if (lo < 0 || hi < lo || hi > a.rows) lo = hi = 0;
             v.e = e;
-            v.m0 = (r % mt) * 128;
+            v.m0 = (r % mt) * (128 * CG);
             v.c0 = (r / mt) * NB;
             v.n = min(NB, a.N - v.c0);
             v.k0 = lo;
             v.steps = (hi - lo + 63) / 64;
             v.tail = hi - lo - (v.steps - 1) * 64;
-            u += gridDim.x;
+            u += gridDim.x / CG;
         } else {
             RowUnit w;
             if (!rows.next(w)) return false;
-            v = {w.e, w.m0, w.r0, w.n, 0, (a.K + 63) / 64, 64};
+            v = {w.e, w.m0, w.r0, w.n, 0, 0, 0, 0, (a.K + 63) / 64, 64};
         }
+        v.m0 += 128 * rank;
+        // whole 64-column chunks where the columns are MN-major
+        v.nh = CG == 1 ? (v.n + 15) & ~15 : MODE == DW ? (v.n + 127) / 128 * 64 : (v.n + 31) / 32 * 16;
+        v.cb = v.c0 + v.nh * rank;
+        v.nb = max(0, min(v.nh, v.n - v.nh * rank));
         return true;
     }
 };
@@ -110,29 +125,18 @@ __device__ __forceinline__ void put(uint16_t* p, uint32_t d) { *p = f32_to_bf16_
 template <class T>
 __device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int n, bool mine)
 {
-    uint32_t d[16];
-    int c = 0;
-    for (; c + 16 <= n; c += 16) {
+    for (int c = 0; c < n; c += 16) {
+        uint32_t d[16];
         tmem_ld16(src + c, d);
         wait_ld();
         if (mine) {
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-                put(p, d[j]);
+                if (c + j < n) put(p, d[j]);
                 p += ldo;
             }
         }
         __syncwarp();   // the warp's next tensor-memory load is a converged one
-    }
-    if (c < n) {
-        tmem_ld16(src + c, d);
-        wait_ld();
-        if (mine) {
-#pragma unroll
-            for (int j = 0; j < 16; j++)
-                if (c + j < n) put(p + j * ldo, d[j]);
-        }
-        __syncwarp();
     }
 }
 
@@ -163,15 +167,17 @@ __device__ __forceinline__ void add_row16(uint16_t* p, const uint32_t (&d)[16], 
     }
 }
 
-template <int MODE, int NB>
+template <int MODE, int NB, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
               const __grid_constant__ CUtensorMap tm_out, const Args a)
 {
-    constexpr int STAGE = kABytes + NB * 128;
-    constexpr uint32_t TMEM = 2 * NB < 32 ? 32 : 2 * NB;
+    constexpr int STAGE = kABytes + NB / CG * 128;
+    constexpr uint32_t TMEM = 2 * NB;
+    constexpr bool RELAY = MODE == DW || CG == 2;
+    constexpr bool PAIR = CG == 2;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
+    __shared__ __align__(8) uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
     __shared__ uint32_t s_tmem;
     __shared__ volatile long long s_issued[2];
     __shared__ int s_abort, s_scan[2 * kThreads / 32];
@@ -180,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     LiveExpert* tab = reinterpret_cast<LiveExpert*>(staging + (MODE == DW ? kStaging : 0));
     int* off = reinterpret_cast<int*>(tab);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
     volatile int* abort_v = &s_abort;
     int* err = &g_gemm_error;
 
@@ -187,11 +194,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_abort = 0;
         for (int i = 0; i < a.stages; i++) {
             mbar_init(smem_u32(&full[i]), 2);   // both copy warps
+            mbar_init(smem_u32(&ready[i]), CG);
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), 4);
+            mbar_init(smem_u32(&acc_empty[i]), 4 * CG);
         }
         mbar_init(smem_u32(&fin), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -199,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         tma_prefetch(&tm_a);
     } else if (warp == 2) {
-        for (int i = 0; i < kRowMaps && a.box << i <= NB; i++) tma_prefetch(&tm_b.m[i]);
+        for (int i = 0; i < kRowMaps && a.box << i <= NB / CG; i++) tma_prefetch(&tm_b.m[i]);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), TMEM);
+    if (warp == 1) tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);
     fence_before();
     int live = 0;
     if (MODE == DW) {
@@ -210,114 +218,148 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         live = build_live(a.offsets, a.E, a.rows, NB, tab, s_scan);
     }
+    if (PAIR) cluster_sync();   // the peer's barriers exist
     fence_after();
     const uint32_t tmem = s_tmem;
-    Units<MODE, NB> units(a, tab, off, live);
+    Units<MODE, NB, CG> units(a, tab, off, live, rank);
     Unit v;
 
     if (warp == 0 || warp == 2) {
-        // ============ copies: warp 0 the features (A), warp 2 the columns (B);
-        // the whole warp walks the loop, one elected lane issues
+        // ============ copies: warp 0 the features (A), warp 2 the columns (B)
         const bool is_a = warp == 0;
-        int st = 0, withheld = -1;
-        uint32_t ph = 0;
-        long long issued = 0;
-        bool ok = true;
-        while (ok && units.next(v)) {
-            const int ub = MODE == DW ? (a.chunks_b ? NB / 64 : (v.n + 63) / 64) : row_units(v.n, a.box);
-            const uint32_t bytes = is_a ? kABytes : (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
-            for (int s = 0; s < v.steps; s++) {
-                if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
-                const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
-                const int k = v.k0 + 64 * s;
-                if (a.withhold && blockIdx.x == 0 && issued == 0) {
-                    withheld = st;   // testing: never filled, so the wait for it runs out
-                } else if (is_a) {
-                    mbar_expect_tx(bar, bytes);
-                    if (MODE == FWD) {
-                        tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
-                    } else if (MODE == DX) {
-                        if (a.chunks_a) {
-                            tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
+        if (elect1()) {
+            int st = 0;
+            uint32_t ph = 0;
+            long long issued = 0;
+            bool ok = true;
+            while (ok && units.next(v)) {
+                const int ub = MODE == DW ? (a.chunks_b ? NB / CG / 64 : (v.nh + 63) / 64) : row_units(v.nb, a.box);
+                const uint32_t bytes = is_a ? kABytes : (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
+                for (int s = 0; s < v.steps; s++) {
+                    if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
+                    const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
+                    const int k = v.k0 + 64 * s;
+                    if (a.withhold && blockIdx.x == 0 && issued == 0) {
+                        // testing: never filled, so the wait for it runs out
+                    } else if (is_a) {
+                        mbar_expect_tx(bar, bytes);
+                        if (MODE == FWD) {
+                            tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
+                        } else if (MODE == DX) {
+                            if (a.chunks_a) {
+                                tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
+                            } else {
+                                tma_3d(sa, &tm_a, v.m0, k, v.e, bar);
+                                tma_3d(sa + 8192, &tm_a, v.m0 + 64, k, v.e, bar);
+                            }
+                        } else if (a.chunks_a) {
+                            tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
                         } else {
-                            tma_3d(sa, &tm_a, v.m0, k, v.e, bar);
-                            tma_3d(sa + 8192, &tm_a, v.m0 + 64, k, v.e, bar);
+                            tma_2d(sa, &tm_a, v.m0, k, bar);
+                            tma_2d(sa + 8192, &tm_a, v.m0 + 64, k, bar);
                         }
-                    } else if (a.chunks_a) {
-                        tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
+                    } else if (bytes == 0) {
+                        mbar_arrive(bar);   // a pair's second half without columns
                     } else {
-                        tma_2d(sa, &tm_a, v.m0, k, bar);
-                        tma_2d(sa + 8192, &tm_a, v.m0 + 64, k, bar);
+                        mbar_expect_tx(bar, bytes);
+                        if (MODE != DW)
+                            tma_rows(sb, tm_b, k, v.cb, ub, a.box, bar);
+                        else if (a.chunks_b)
+                            tma_3d(sb, &tm_b.m[0], 0, k, v.cb / 64, bar);
+                        else
+                            for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.cb + 64 * i, k, bar);
                     }
-                } else {
-                    mbar_expect_tx(bar, bytes);
-                    if (MODE != DW)
-                        tma_rows(sb, tm_b, k, v.c0, ub, a.box, bar);
-                    else if (a.chunks_b)
-                        tma_3d(sb, &tm_b.m[0], 0, k, v.c0 / 64, bar);
-                    else
-                        for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.c0 + 64 * i, k, bar);
+                    issued++;
+                    if (++st == a.stages) { st = 0; ph ^= 1; }
                 }
-                issued++;
-                if (++st == a.stages) { st = 0; ph ^= 1; }
             }
+            s_issued[is_a] = issued;
         }
+        __syncwarp();
         // Every issued copy lands before the CTA exits.  After an abort one warp
         // may be ahead: the other arrives for the stages it did not fill, so
         // that their phases complete with the copies in flight.
-        if (lane == 0) s_issued[is_a] = issued;
         asm volatile("bar.sync 1, 64;" ::: "memory");
-        const long long most = max(s_issued[0], s_issued[1]);
+        const long long mine = s_issued[is_a], most = max(mine, s_issued[!is_a]);
         if (lane == 0)
-            for (long long i = issued; i < most; i++) mbar_arrive(smem_u32(&full[i % a.stages]));
+            for (long long i = mine; i < most; i++) mbar_arrive(smem_u32(&full[i % a.stages]));
+        const bool withheld = a.withhold && blockIdx.x == 0;   // its stage 0 never completes
         if (is_a)
             for (long long i = most > a.stages ? most - a.stages : 0; i < most; i++)
-                if ((int)(i % a.stages) != withheld)
+                if (i > 0 || !withheld)
                     mbar_drain(smem_u32(&full[i % a.stages]), (uint32_t)(i / a.stages) & 1, err);
     } else if (warp == 1) {
         // ============ MMAs
-        int st = 0, it = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok && units.next(v)) {
-            if (v.steps == 0) continue;   // DW: an expert without rows
-            const int ab = it & 1;
-            if (it >= 2) {   // the epilogue has read this accumulator's previous unit
-                if (!(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err))) break;
-                fence_after();
-            }
-            const uint32_t d = tmem + (uint32_t)(ab * NB);
-            const uint32_t id = idesc_bf16((v.n + 15) & ~15, MODE != FWD, MODE == DW);
-            for (int s = 0; s < v.steps; s++) {
-                if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
-                unsigned char* sp = ring + (size_t)st * STAGE;
-                int kk = 4;
-                if (MODE == DW && s == v.steps - 1 && v.tail < 64) {
-                    // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
-                    kk = (v.tail + 15) / 16;
-                    const int z = 128 * (16 * kk - v.tail), chunks = 2 + (v.n + 63) / 64;
-                    for (int i = 16 * lane; i < z; i += 512)
-                        for (int c = 0; c < chunks; c++)
-                            *reinterpret_cast<uint4*>(sp + 8192 * c + 128 * v.tail + i) = make_uint4(0, 0, 0, 0);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
+        if (rank == 0) {
+            if (elect1()) {
+                int st = 0, it = 0;
+                uint32_t ph = 0;
+                bool ok = true;
+                while (ok && units.next(v)) {
+                    if (v.steps == 0) continue;   // DW: an expert without rows
+                    const int ab = it & 1;
+                    if (it >= 2) {   // the epilogue has read this accumulator's previous unit
+                        if (!(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
+                            break;
+                        fence_after();
+                    }
+                    const uint32_t d = tmem + (uint32_t)(ab * NB);
+                    const uint32_t id = idesc_bf16<CG>(CG * v.nh, MODE != FWD, MODE == DW);
+                    for (int s = 0; s < v.steps; s++) {
+                        const uint32_t bar = smem_u32(RELAY ? &ready[st] : &full[st]);
+                        if (!(ok = mbar_wait(bar, ph, abort_v, a.wait, err))) break;
+                        fence_after();
+                        const uint32_t sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
+                        const uint64_t da = MODE == FWD ? desc_k(sa) : desc_mn(sa, 8192);
+                        const uint64_t db = MODE == DW ? desc_mn(sb, 8192) : desc_k(sb);
+                        // 16 inner indices: 32 bytes along a K-major row, 16 rows MN-major
+                        const int kk = MODE == DW && s == v.steps - 1 ? (v.tail + 15) / 16 : 4;
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (MODE != DW || k < kk)
+                                mma_bf16<CG>(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id,
+                                             s > 0 || k > 0);
+                        commit<CG>(smem_u32(&empty[st]));   // the stage is free once these MMAs have read it
+                        if (++st == a.stages) { st = 0; ph ^= 1; }
+                    }
+                    if (!ok) break;
+                    commit<CG>(smem_u32(&acc_full[ab]));
+                    it++;
                 }
-                fence_after();
-                const uint32_t sa = smem_u32(sp), sb = sa + kABytes;
-                const uint64_t da = MODE == FWD ? desc_k(sa) : desc_mn(sa, 8192);
-                const uint64_t db = MODE == DW ? desc_mn(sb, 8192) : desc_k(sb);
-                for (int k = 0; k < kk; k++)   // 16 inner indices: 32 bytes along a K-major row, 16 rows MN-major
-                    mma_bf16(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id, s > 0 || k > 0);
-                commit(smem_u32(&empty[st]));   // the stage is free once these MMAs have read it
-                if (++st == a.stages) { st = 0; ph ^= 1; }
+                commit<CG>(smem_u32(&fin));   // every MMA completes before tensor memory is released
+                mbar_drain(smem_u32(&fin), 0, err);
             }
-            if (!ok) break;
-            commit(smem_u32(&acc_full[ab]));
-            it++;
+            __syncwarp();
         }
-        commit(smem_u32(&fin));   // every MMA completes before tensor memory is released
-        mbar_drain(smem_u32(&fin), 0, err);
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        // ============ between copies and MMAs
+        if (RELAY) {
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && units.next(v)) {
+                for (int s = 0; s < v.steps; s++) {
+                    if (!(ok = mbar_wait_warp(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
+                    if (MODE == DW && s == v.steps - 1 && (v.tail & 15)) {
+                        // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
+                        unsigned char* p = ring + (size_t)st * STAGE + 128 * v.tail;
+                        const int z = 128 * (16 - (v.tail & 15)), chunks = 2 + (v.nh + 63) / 64;
+                        for (int i = 16 * lane; i < z; i += 512)
+                            for (int c = 0; c < chunks; c++)
+                                *reinterpret_cast<uint4*>(p + 8192 * c + i) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async;" ::: "memory");
+                        if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&ready[st]), 0));
+                        else mbar_arrive(smem_u32(&ready[st]));
+                    }
+                    if (++st == a.stages) { st = 0; ph ^= 1; }
+                }
+            }
+        }
+    } else {
         // ============ epilogue: lane quarter q = warp % 4, one feature per thread
         const int q = warp & 3;
         int it = 0, turn = 0;
@@ -327,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool none = MODE == DW && v.steps == 0;   // an expert without rows: its gradient is zero
             if (none && a.accumulate) continue;
             if (!none) {
-                if (!(ok = mbar_wait(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+                if (!(ok = mbar_wait_warp(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
                 fence_after();
             }
             const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
@@ -392,23 +434,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&acc_empty[ab]), 0));
+                else mbar_arrive(smem_u32(&acc_empty[ab]));
+            }
             it++;
         }
         if (MODE == DW && lane == 0) bulk_wait();   // the staging tiles are read, the stores done
     }
     fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();   // nothing of the peer reads this CTA's shared or tensor memory any more
     if (warp == 1) {
         fence_after();
-        tmem_dealloc(tmem, TMEM);
+        tmem_dealloc<CG>(tmem, TMEM);
     }
+    if (PAIR) cluster_sync();
 }
 
-template <int MODE, int NB>
+template <int MODE, int NB, int CG>
 int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, cudaStream_t st)
 {
-    constexpr int STAGE = kABytes + NB * 128;
+    constexpr int STAGE = kABytes + NB / CG * 128;
     int sms = 0;
     if (int rc = device_sms(&sms)) return rc;
     const int table = (int)align_up(MODE == DW ? sizeof(int) * (a.E + 1) : sizeof(LiveExpert) * (a.E + 1), 128);
@@ -416,12 +463,22 @@ int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorM
     a.stages = (kSmemMax - 1024 - fixed) / STAGE;                    // 1 KB static
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = fixed + a.stages * STAGE;
-    auto* kern = gg_kernel<MODE, NB>;
+    auto* kern = gg_kernel<MODE, NB, CG>;
     MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    kern<<<sms, kThreads, smem, st>>>(ta, tb, to, a);
-    MOE_LAUNCH_CHECK();
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms / CG * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CG == 2 ? 1 : 0;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, ta, tb, to, a));
     return MOE_OK;
 }
 
@@ -472,9 +529,9 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     }
     const bool small = rows <= 16 * (int64_t)E;
     a.box = small ? 16 : 32;
-    if (!encode_rows(&tb, E_BF16, x, ldx, a.K, rows, a.box, small ? 32 : 256)) return MOE_ERR_CUDA;
+    if (!encode_rows(&tb, E_BF16, x, ldx, a.K, rows, a.box, small ? 32 : 128)) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return small ? launch_nb<MODE, 32>(a, ta, tb, ta, st) : launch_nb<MODE, 256>(a, ta, tb, ta, st);
+    return small ? launch_nb<MODE, 32, 1>(a, ta, tb, ta, st) : launch_nb<MODE, 256, 2>(a, ta, tb, ta, st);
 }
 
 }  // namespace
@@ -588,9 +645,9 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     const int size = dtype_size(dw_dtype);
     const uint64_t strides[2] = {(uint64_t)in * size, (uint64_t)in * out * size};
     const uint32_t box[3] = {128u / size, 32, 1};
-    if (!map_mn(&ta, &a.chunks_a, d_dy, lddy, out, rows, 2, 0) || !map_mn(&tb.m[0], &a.chunks_b, d_x, ldx, in, rows, 4, 0) ||
+    if (!map_mn(&ta, &a.chunks_a, d_dy, lddy, out, rows, 2, 0) || !map_mn(&tb.m[0], &a.chunks_b, d_x, ldx, in, rows, 2, 0) ||
         !encode_map(&to, a.out_f32 ? E_F32 : E_BF16, 3, d_dw, dims, strides, box))
         return MOE_ERR_CUDA;
-    a.box = 256;   // one map of the columns
-    return launch_nb<DW, 256>(a, ta, tb, to, st);
+    a.box = 128;   // one map of the columns
+    return launch_nb<DW, 256, 2>(a, ta, tb, to, st);
 }

@@ -91,12 +91,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch(&tm_a);
         for (int i = 0; i < kRowMaps && a.box << i <= NB; i++) tma_prefetch(&tm_b.m[i]);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&s_tmem), TMEM);
+    if (warp == 1) tmem_alloc<1>(smem_u32(&s_tmem), TMEM);
     fence_before();
     const int live = build_live(a.offsets, a.E, a.rows, NB, tab, s_scan);
     fence_after();
     const uint32_t tmem = s_tmem;
-    RowUnits<NB> units(tab, live, a.M);
+    RowUnits<NB, 1> units(tab, live, a.M);
     RowUnit v;
 
     if (warp == 0) {
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         long long issued = 0;
         bool ok = true;
+        if (elect1()) {
         while (ok && units.next(v)) {
             const int ub = row_units(v.n, a.box);
             const uint32_t bytes = kABytes + (uint32_t)(ub * a.box * 128);
@@ -125,13 +126,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every issued copy lands before the CTA exits
         for (int i = 0; i < a.stages && i < issued; i++)
             if (i != withheld) mbar_drain(smem_u32(&full[i]), i < st ? ph : (ph ^ 1), err);
+        }
+        __syncwarp();
     } else if (warp == 1) {
         // ============ MMAs: one accumulator per block
         int st = 0, buf = 0;
         uint32_t ph = 0, bph = 0;
         bool ok = true;
+        if (elect1()) {
         while (ok && units.next(v)) {
-            const uint32_t id = idesc_e4m3((v.n + 15) & ~15);
+            const uint32_t id = idesc_e4m3<1>((v.n + 15) & ~15);
             for (int b = 0; b < a.blocks; b++) {
                 if (!(ok = mbar_wait(smem_u32(&acc_empty[buf]), bph ^ 1, abort_v, a.wait, err))) break;
                 if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
@@ -139,15 +143,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t sa = smem_u32(ring + (size_t)st * STAGE);
                 const uint64_t da = desc_k(sa), db = desc_k(sa + kABytes);
 #pragma unroll
-                for (int k = 0; k < 4; k++) mma_e4m3(tmem + (uint32_t)(buf * NB), da + 2 * k, db + 2 * k, id, k > 0);
-                commit(smem_u32(&empty[st]));
-                commit(smem_u32(&acc_full[buf]));
+                for (int k = 0; k < 4; k++) mma_e4m3<1>(tmem + (uint32_t)(buf * NB), da + 2 * k, db + 2 * k, id, k > 0);
+                commit<1>(smem_u32(&empty[st]));
+                commit<1>(smem_u32(&acc_full[buf]));
                 if (++st == a.stages) { st = 0; ph ^= 1; }
                 if (++buf == kBufs) { buf = 0; bph ^= 1; }
             }
         }
-        commit(smem_u32(&fin));
+        commit<1>(smem_u32(&fin));
         mbar_drain(smem_u32(&fin), 0, err);
+        }
+        __syncwarp();
     } else if (warp < 4) {
         // ============ scales: xs * ws of four blocks by NB rows per slot
         constexpr int PER = kGroup * NB / 64;
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (b < a.blocks && c < v.n)
                         s[i] = __ldg(a.xs + (int64_t)b * a.rows + v.r0 + c) * __ldg(wsp + b);
                 }
-                if (!(ok = mbar_wait(smem_u32(&sc_empty[slot]), ph ^ 1, abort_v, a.wait, err))) break;
+                if (!(ok = mbar_wait_warp(smem_u32(&sc_empty[slot]), ph ^ 1, abort_v, a.wait, err))) break;
 #pragma unroll
                 for (int i = 0; i < PER; i++) (&s_scale[slot][0][0])[t + 64 * i] = s[i];
                 __syncwarp();
@@ -187,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = CW * half;
             for (int b = 0; b < a.blocks; b++) {
                 const int g = b % kGroup;
-                if (g == 0 && !(ok = mbar_wait(smem_u32(&sc_full[slot]), sph, abort_v, a.wait, err))) break;
-                if (!(ok = mbar_wait(smem_u32(&acc_full[buf]), bph, abort_v, a.wait, err))) break;
+                if (g == 0 && !(ok = mbar_wait_warp(smem_u32(&sc_full[slot]), sph, abort_v, a.wait, err))) break;
+                if (!(ok = mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort_v, a.wait, err))) break;
                 fence_after();
                 const uint32_t src = tmem + (uint32_t)(buf * NB + c0) + ((uint32_t)(32 * q) << 16);
 #pragma unroll
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         fence_after();
-        tmem_dealloc(tmem, TMEM);
+        tmem_dealloc<1>(tmem, TMEM);
     }
 }
 

@@ -1,7 +1,8 @@
 // Tensor-core (tcgen05), TMA and mbarrier wrappers of the expert matrix
-// products (grouped_gemm.cu, grouped_gemm_fp8.cu).  The issuing wrappers are
-// called by converged warps: every lane computes the operands, one lane
-// elected by elect.sync issues.
+// products (grouped_gemm.cu, grouped_gemm_fp8.cu).  Copies, MMAs and commits
+// are issued by one thread, the one elect1() picks in its warp, which walks
+// its role's loop alone: against a warp-wide loop with an election per
+// instruction four MMAs take 61 cycles to issue instead of 163.
 #pragma once
 
 #include <cuda.h>
@@ -15,6 +16,42 @@ constexpr long long kWaitCycles = 4000000000ll;   // ~2 s: drains, and waits unl
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// True for one lane of a converged warp.
+__device__ __forceinline__ bool elect1()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// ------------------------------------------------------------------ clusters (CTA pairs)
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The cluster address of `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// One arrival by the calling lane on a barrier anywhere in the cluster.  What
+// it announces was written by the async proxy (copies) or read from tensor
+// memory; a release at cluster scope, which waits for every earlier store of
+// the thread, is left to callers with writes of their own to publish.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // ------------------------------------------------------------------ mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
@@ -22,8 +59,7 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 // One arrival by the calling lane.
@@ -34,32 +70,36 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok)
-                 : "r"(bar), "r"(parity), "n"(20000)
+                 : "r"(bar), "r"(parity)
                  : "memory");
     return ok != 0;
 }
-// Bounded wait of a whole warp: false when another role raised the abort
-// flag, or after `limit` cycles, in which case it raises the flag itself and
-// records MOE_ERR_TIMEOUT in *error.
+// Bounded wait: false when another role raised the CTA's abort flag, or after
+// `limit` cycles, in which case it raises the flag itself and records
+// MOE_ERR_TIMEOUT in *error.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit,
                                           int* error)
 {
-    bool ok = mbar_try(bar, parity);
-    if (!ok) {
-        const long long t0 = clock64();
-        while (!(ok = mbar_try(bar, parity))) {
-            if (*abort_flag) break;
-            if (clock64() - t0 > limit) {
-                *abort_flag = 1;
-                atomicCAS(error, 0, (int)MOE_ERR_TIMEOUT);
-                break;
-            }
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            *abort_flag = 1;
+            atomicCAS(error, 0, (int)MOE_ERR_TIMEOUT);
+            return false;
         }
     }
-    return __all_sync(0xffffffffu, ok);
+    return true;
+}
+// The same for a converged warp: every lane gets the same answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit,
+                                               int* error)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, error));
 }
 // Drain wait for this CTA's own copies or MMAs before it exits: bounded by
 // time only.
@@ -80,23 +120,20 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* m)
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar)
 {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar)
 {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar)
 {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
                  : "memory");
 }
 // Stores of a converged warp's own tiles: ordered by one lane's bulk groups,
@@ -122,21 +159,38 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// One arrival on `bar` once every MMA issued so far has finished; for a pair
+// (CG = 2) on the barrier at that address in both CTAs.
+template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-                 : "memory");
+    if (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+                         "r"(bar), "h"((uint16_t)3)
+                     : "memory");
 }
-// `cols` (a power of two >= 32) tensor-memory columns; the address lands in *slot.
+// `cols` (a power of two >= 32) tensor-memory columns, in both CTAs of a
+// pair; the address lands in *slot.
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
 }
+template <int CG>
 __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
 // Shared-memory descriptors in the 128-byte swizzle.  K-major: rows of 128
@@ -153,29 +207,40 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t chunk)
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// Instruction descriptor, fp32 accumulators, M = 128, N = n (a multiple of
-// 16): bf16 operands (kind::f16) with either operand MN-major, or e4m3
+// Instruction descriptor, fp32 accumulators, M = 128 CG, N = n (a multiple of
+// 16 CG): bf16 operands (kind::f16) with either operand MN-major, or e4m3
 // (kind::f8f6f4, K-major, every format field 0).
+template <int CG>
 __device__ __forceinline__ uint32_t idesc_bf16(int n, bool a_mn, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(n >> 3) << 17) | (8u << 24);
+           ((uint32_t)(n >> 3) << 17) | (8u * CG << 24);
 }
-__device__ __forceinline__ uint32_t idesc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
+template <int CG>
+__device__ __forceinline__ uint32_t idesc_e4m3(int n)
+{
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u * CG << 24);
+}
 
-// D[tmem] (+)= A[smem] B[smem], K = 16 bf16 or 32 e4m3 columns.
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
+// D[tmem] (+)= A[smem] B[smem], K = 16 bf16 or 32 e4m3 columns.  A pair's MMA
+// is issued by its first CTA: each CTA holds 128 rows of A, half of B's N rows
+// and the accumulator of its own 128 rows, all at the same addresses.
+#define MOE_TC_MMA(name, kind)                                                                                    \
+    template <int CG>                                                                                             \
+    __device__ __forceinline__ void name(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)        \
+    {                                                                                                             \
+        if (CG == 1)                                                                                              \
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                       \
+                         "tcgen05.mma.cta_group::1.kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d),            \
+                         "l"(a), "l"(b), "r"(idesc), "r"(acc));                                                   \
+        else                                                                                                      \
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                       \
+                         "tcgen05.mma.cta_group::2.kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d),            \
+                         "l"(a), "l"(b), "r"(idesc), "r"(acc));                                                   \
+    }
+MOE_TC_MMA(mma_bf16, "f16")
+MOE_TC_MMA(mma_e4m3, "f8f6f4")
+#undef MOE_TC_MMA
 
 // 16 consecutive columns of the warp's 32 lanes (32 * (warp % 4) on).
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v)
@@ -286,23 +351,23 @@ __device__ __forceinline__ int build_live(const int32_t* __restrict__ offsets, i
     return live;
 }
 
-// A tile of the row products: 128 features from m0 on, n rows from r0 on, of
-// expert e's matrix.
+// A tile of the row products: 128 features (256 for a pair of CTAs) from m0
+// on, n rows from r0 on, of expert e's matrix.
 struct RowUnit {
     int e, m0, r0, n;
 };
 
-// The tiles of a CTA: u = blockIdx.x, blockIdx.x + gridDim.x, ... .  An
+// The tiles of a CTA or pair: u = its number, then every grid's worth on.  An
 // expert's token blocks run fastest, then its feature tiles, so that CTAs
 // running together share weight tiles and rows in L2.
-template <int NB>
+template <int NB, int CG>
 struct RowUnits {
     const LiveExpert* tab;
     int live, mt;
     long long u, total;
 
     __device__ RowUnits(const LiveExpert* t, int live_, int M)
-        : tab(t), live(live_), mt((M + 127) / 128), u(blockIdx.x), total((long long)t[live_].pre * mt)
+        : tab(t), live(live_), mt((M + 128 * CG - 1) / (128 * CG)), u(blockIdx.x / CG), total((long long)t[live_].pre * mt)
     {
     }
     __device__ bool next(RowUnit& v)
@@ -318,10 +383,10 @@ struct RowUnits {
         const long long r = u - (long long)L.pre * mt;
         const int nt = (L.r1 - L.r0 + NB - 1) / NB;
         v.e = L.e;
-        v.m0 = (int)(r / nt) * 128;
+        v.m0 = (int)(r / nt) * (128 * CG);
         v.r0 = L.r0 + (int)(r % nt) * NB;
         v.n = min(NB, L.r1 - v.r0);
-        u += gridDim.x;
+        u += gridDim.x / CG;
         return true;
     }
 };

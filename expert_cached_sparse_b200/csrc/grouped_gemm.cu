@@ -73,46 +73,67 @@ struct Unit {
     int tail;           // DW: valid rows of the last step
 };
 
-// The units of a CTA or pair.  DW: every expert's tiles, feature tiles fastest.
+// The tiles of a CTA or pair.
 template <int MODE, int NB, int CG>
 struct Units {
     const Args& a;
-    RowUnits<NB, CG> rows;
-    const int* off;          // DW: offsets in shared memory
+    PlanWalk walk;
     const int rank;
-    long long u, total;
 
-    __device__ Units(const Args& a_, const LiveExpert* t, const int* o, int live, int rank_)
-        : a(a_), rows(t, live, a_.M), off(o), rank(rank_), u(blockIdx.x / CG),
-          total((long long)a_.E * ((a_.M + 128 * CG - 1) / (128 * CG)) * ((a_.N + NB - 1) / NB))
+    __device__ Units(const Args& a_, const PlanExpert* tab, const int*, int live, int rank_)
+        : a(a_), walk(tab, live, {NB}, (a_.M + 128 * CG - 1) / (128 * CG), blockIdx.x / CG, gridDim.x / CG), rank(rank_)
     {
     }
-    __device__ bool next(Unit& v)
+    __device__ __forceinline__ bool next(Unit& v)
     {
-        if (MODE == DW) {
-            if (u >= total) return false;
-            const int mt = (a.M + 128 * CG - 1) / (128 * CG), per = mt * ((a.N + NB - 1) / NB);
-            const int e = (int)(u / per), r = (int)(u % per);
-            int lo = off[e], hi = off[e + 1];
-            if (lo < 0 || hi < lo || hi > a.rows) lo = hi = 0;
-            v.e = e;
-            v.m0 = (r % mt) * (128 * CG);
-            v.c0 = (r / mt) * NB;
-            v.n = min(NB, a.N - v.c0);
-            v.k0 = lo;
-            v.steps = (hi - lo + 63) / 64;
-            v.tail = hi - lo - (v.steps - 1) * 64;
-            u += gridDim.x / CG;
-        } else {
-            RowUnit w;
-            if (!rows.next(w)) return false;
-            v = {w.e, w.m0, w.r0, w.n, 0, 0, 0, 0, (a.K + 63) / 64, 64};
-        }
-        v.m0 += 128 * rank;
-        // whole 64-column chunks where the columns are MN-major
-        v.nh = CG == 1 ? (v.n + 15) & ~15 : MODE == DW ? (v.n + 127) / 128 * 64 : (v.n + 31) / 32 * 16;
+        PlanTile w;
+        if (!walk.next(w)) return false;
+        v.e = w.e;
+        v.m0 = (w.m * CG + rank) * 128;
+        v.c0 = w.r0;
+        v.n = w.n;
+        v.k0 = 0;
+        v.steps = (a.K + 63) / 64;
+        v.tail = 64;
+        v.nh = mma_rows<CG>(v.n) / CG;
         v.cb = v.c0 + v.nh * rank;
         v.nb = max(0, min(v.nh, v.n - v.nh * rank));
+        return true;
+    }
+};
+
+// A weight gradient's tiles: every expert's, an expert's feature tiles
+// fastest.  (A pair of CTAs gains it nothing: its way out takes longest.)
+template <int NB>
+struct Units<DW, NB, 1> {
+    const Args& a;
+    const int* off;   // the offsets, in shared memory
+    const int mt, per;
+    long long u, total;
+
+    __device__ Units(const Args& a_, const PlanExpert*, const int* o, int, int)
+        : a(a_), off(o), mt((a_.M + 127) / 128), per(mt * ((a_.N + NB - 1) / NB)), u(blockIdx.x),
+          total((long long)a_.E * per)
+    {
+    }
+    __device__ __forceinline__ bool next(Unit& v)
+    {
+        if (u >= total) return false;
+        // a 64-bit division takes hundreds of cycles
+        v.e = total < 0x7fffffff ? (int)u / per : (int)(u / per);
+        const int r = (int)(u - (long long)v.e * per);
+        int lo = off[v.e], hi = off[v.e + 1];
+        if (lo < 0 || hi < lo || hi > a.rows) lo = hi = 0;
+        v.m0 = r % mt * 128;
+        v.c0 = r / mt * NB;
+        v.n = min(NB, a.N - v.c0);
+        v.k0 = lo;
+        v.steps = (hi - lo + 63) / 64;
+        v.tail = hi - lo - (v.steps - 1) * 64;
+        v.nh = mma_rows<1>(v.n);
+        v.cb = v.c0;
+        v.nb = v.n;
+        u += gridDim.x;
         return true;
     }
 };
@@ -128,7 +149,7 @@ __device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int 
     for (int c = 0; c < n; c += 16) {
         uint32_t d[16];
         tmem_ld16(src + c, d);
-        wait_ld();
+        wait_ld(d);
         if (mine) {
 #pragma unroll
             for (int j = 0; j < 16; j++) {
@@ -180,16 +201,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
     __shared__ uint32_t s_tmem;
     __shared__ volatile long long s_issued[2];
-    __shared__ int s_abort, s_scan[2 * kThreads / 32];
-    unsigned char* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    __shared__ int s_abort;
+    __shared__ long long s_scan[kThreads / 32];
+    unsigned char* ring = smem_raw;
     unsigned char* staging = ring + (size_t)a.stages * STAGE;   // DW: 4 warps x 2 tiles of 32 rows x 128 bytes
-    LiveExpert* tab = reinterpret_cast<LiveExpert*>(staging + (MODE == DW ? kStaging : 0));
+    PlanExpert* tab = reinterpret_cast<PlanExpert*>(staging + (MODE == DW ? kStaging : 0));
     int* off = reinterpret_cast<int*>(tab);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = PAIR ? (int)cluster_rank() : 0;
     volatile int* abort_v = &s_abort;
     int* err = &g_gemm_error;
 
+    if (smem_u32(ring) & 1023) {   // the swizzle counts on it; static shared memory is padded so
+        if (tid == 0) atomicCAS(err, 0, (int)MOE_ERR_UNSUPPORTED);
+        return;
+    }
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < a.stages; i++) {
@@ -216,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = tid; i <= a.E; i += kThreads) off[i] = __ldg(a.offsets + i);
         __syncthreads();
     } else {
-        live = build_live(a.offsets, a.E, a.rows, NB, tab, s_scan);
+        live = build_plan(a.offsets, a.E, a.rows, {NB}, tab, s_scan);
     }
     if (PAIR) cluster_sync();   // the peer's barriers exist
     fence_after();
@@ -276,18 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_issued[is_a] = issued;
         }
         __syncwarp();
-        // Every issued copy lands before the CTA exits.  After an abort one warp
-        // may be ahead: the other arrives for the stages it did not fill, so
-        // that their phases complete with the copies in flight.
-        asm volatile("bar.sync 1, 64;" ::: "memory");
-        const long long mine = s_issued[is_a], most = max(mine, s_issued[!is_a]);
-        if (lane == 0)
-            for (long long i = mine; i < most; i++) mbar_arrive(smem_u32(&full[i % a.stages]));
-        const bool withheld = a.withhold && blockIdx.x == 0;   // its stage 0 never completes
-        if (is_a)
-            for (long long i = most > a.stages ? most - a.stages : 0; i < most; i++)
-                if (i > 0 || !withheld)
-                    mbar_drain(smem_u32(&full[i % a.stages]), (uint32_t)(i / a.stages) & 1, err);
+        drain_copies(full, a.stages, s_issued, is_a, a.withhold && blockIdx.x == 0, err);
     } else if (warp == 1) {
         // ============ MMAs
         if (rank == 0) {
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < v.n; c += 16) {
                     uint32_t d[16];
                     tmem_ld16(src + c, d);
-                    wait_ld();
+                    wait_ld(d);
                     if (mine) add_row16(static_cast<uint16_t*>(a.out) + at + c, d, v.n - c);
                     __syncwarp();   // the warp's next tensor-memory load is a converged one
                 }
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (v.m0 + 32 * q < a.M)
                     for (int c = 0; c < v.n; c += w, turn ^= 1) {
                         unsigned char* tile = staging + 8192 * q + 4096 * turn;
-                        if (lane == 0) bulk_wait_read<1>();
+                        if (lane == 0) bulk_wait_read<1>();   // its previous rows are on their way
                         __syncwarp();
                         for (int h = 0; h < w / 32; h++) {
                             uint32_t d[32];
@@ -401,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             } else {
                                 tmem_ld16(src + c + 32 * h, d);
                                 tmem_ld16(src + c + 32 * h + 16, d + 16);
-                                wait_ld();
+                                wait_ld(d);
+                                hold16(d + 16);
                             }
                             unsigned char* row = tile + 128 * lane;
                             if (a.out_f32) {
@@ -458,8 +474,7 @@ int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorM
     constexpr int STAGE = kABytes + NB / CG * 128;
     int sms = 0;
     if (int rc = device_sms(&sms)) return rc;
-    const int table = (int)align_up(MODE == DW ? sizeof(int) * (a.E + 1) : sizeof(LiveExpert) * (a.E + 1), 128);
-    const int fixed = 1024 + (MODE == DW ? kStaging : 0) + table;   // alignment slack, staging tiles, table
+    const int fixed = MODE == DW ? kStaging + (int)align_up(4 * (a.E + 1), 128) : plan_bytes(a.E);
     a.stages = (kSmemMax - 1024 - fixed) / STAGE;                    // 1 KB static
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = fixed + a.stages * STAGE;
@@ -467,18 +482,7 @@ int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorM
     MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms / CG * CG);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
-    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, ta, tb, to, a));
+    MOE_CUDA_TRY(launch_clusters(kern, sms, CG, kThreads, smem, st, ta, tb, to, a));
     return MOE_OK;
 }
 
@@ -645,9 +649,9 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     const int size = dtype_size(dw_dtype);
     const uint64_t strides[2] = {(uint64_t)in * size, (uint64_t)in * out * size};
     const uint32_t box[3] = {128u / size, 32, 1};
-    if (!map_mn(&ta, &a.chunks_a, d_dy, lddy, out, rows, 2, 0) || !map_mn(&tb.m[0], &a.chunks_b, d_x, ldx, in, rows, 2, 0) ||
+    if (!map_mn(&ta, &a.chunks_a, d_dy, lddy, out, rows, 2, 0) || !map_mn(&tb.m[0], &a.chunks_b, d_x, ldx, in, rows, 4, 0) ||
         !encode_map(&to, a.out_f32 ? E_F32 : E_BF16, 3, d_dw, dims, strides, box))
         return MOE_ERR_CUDA;
-    a.box = 128;   // one map of the columns
-    return launch_nb<DW, 256, 2>(a, ta, tb, to, st);
+    a.box = 256;   // one map of the columns
+    return launch_nb<DW, 256, 1>(a, ta, tb, to, st);
 }

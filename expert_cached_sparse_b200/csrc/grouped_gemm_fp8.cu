@@ -6,17 +6,22 @@
 // The scales are arbitrary, so they cannot go into the tensor core (its block
 // scales are powers of two): each 128-column block is a product of its own in
 // tensor memory, and the epilogue adds it, scaled, to fp32 sums in registers.
-// With 128 features of one weight block as the tensor core's M and NB rows as
-// its N, a block's weight scale is one number per tile and a row's scale one
-// number per column, so the two multiply once per column and each element
-// costs a single FMA.  An expert's rows are never padded beyond 16.
+// Rows are the tensor core's M, one tensor-memory lane and one thread each,
+// and features its N: a thread's scale xs ws is then one number for all of its
+// columns, and an element costs one FMA.  (With features as M and rows as N,
+// as in grouped_gemm.cu, every column has its own scale, and reading those
+// from shared memory takes as long as the FMAs: 575 against 329 cycles for
+// 128 x 256 elements, 16 warps.)  An expert of few rows computes 128 all the
+// same, but 128 x 128 x 128 take 256 cycles and the weights' 16 KB come from
+// HBM at the rate of one such tile in 700, and only warps with rows add.
 //
-// One persistent CTA per SM: warp 0 copies (one 128-column block of both
-// operands per stage, TMA into the 128-byte swizzle), warp 1 issues the MMAs
-// of a block into one of four accumulators, warps 2-3 bring the products of
-// scales into a ring in shared memory, four blocks at a time, and warps 4-11
-// (two per tensor-memory lane quarter, half of the columns each) add.  Waits
-// are bounded as in grouped_gemm.cu.
+// Roles, one persistent CTA per SM: warps 0 and 2 copy (one 128-column block
+// of rows and of weights per stage, TMA into the 128-byte swizzle), warp 1
+// issues the MMAs of a block into one of the accumulators, and warps 4-11 add,
+// a quarter of the rows and half of the columns each.  (On pairs of CTAs, as
+// in grouped_gemm.cu, every block's accumulator has to be handed back across
+// the cluster: 1.26 ms against 0.89 for 4096 tokens.)  Waits are bounded as in
+// grouped_gemm.cu.
 #include "tc.cuh"
 
 namespace moe {
@@ -28,12 +33,15 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 384;
-constexpr int kMaxStages = 12;
-constexpr int kABytes = 128 * 128;   // 128 features x 128 columns
-constexpr int kBufs = 4;             // accumulators
-constexpr int kGroup = 4;            // blocks per scale slot
-constexpr int kSlots = 3;
 constexpr int kEpi = 8;              // epilogue warps
+// Registers a thread of the control warps and of the epilogue's where the
+// latter hold 128 sums each: together what the block is launched with,
+// 128 * 72 + 256 * 216 = 384 * 168.
+constexpr int kRegs = 168, kControlRegs = 72, kSumRegs = 216;
+static_assert(128 * kControlRegs + 32 * kEpi * kSumRegs <= kThreads * kRegs, "a larger split never starts");
+
+constexpr int kMaxStages = 12;
+constexpr int kABytes = 128 * 128;   // 128 rows x 128 columns
 
 struct Args {
     const int32_t* offsets;
@@ -42,197 +50,234 @@ struct Args {
     void* out;
     int64_t ldo;
     int out_f32;
+    int wide;          // output rows are 32-byte aligned
     int E, rows;
     int M, blocks;     // features; 128-column blocks
     int stages;
-    int box;           // smallest height of a copy of the row operand
+    int box;           // smallest height of a copy of the rows
     long long wait;    // limit of every bounded wait, in SM clock cycles
     int withhold;      // testing: CTA 0 leaves its first stage unfilled
 };
 
-template <int NB>
-__global__ void __launch_bounds__(kThreads, 1)
-    gg8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b, const Args a)
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
-    constexpr int STAGE = kABytes + NB * 128;
-    constexpr int CW = NB / 2;                    // columns of one epilogue warp
-    constexpr uint32_t TMEM = kBufs * NB;
-    static_assert(CW % 16 == 0, "columns are read 16 at a time");
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A load that stays where it is written, far ahead of its use (the compiler
+// would move a plain one down to the use and wait for it there); 0 if !in.
+__device__ __forceinline__ float fetch_f32(const float* p, bool in)
+{
+    float v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
+                 "@p ld.global.nc.f32 %0, [%1];\n\t}" : "=f"(v) : "l"(p), "r"((int)in));
+    return v;
+}
+
+// 32 adjacent bytes of a row: one whole sector where rows are aligned so.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        uint4* o = static_cast<uint4*>(p);
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Tiles of 128 rows by NF features.
+template <int NF>
+__global__ void __launch_bounds__(kThreads, 1)
+    gg8_kernel(const __grid_constant__ RowMaps tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a)
+{
+    constexpr int STAGE = kABytes + NF * 128;
+    constexpr int BUFS = 512 / NF;                // accumulators
+    constexpr int CW = NF / 2;                    // columns of one epilogue warp
+    constexpr bool SPLIT = CW > 64;               // registers moved from the control warps to the epilogue's
+    constexpr int GROUP = 4;                      // blocks whose scales are fetched together, a group ahead
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kBufs], acc_empty[kBufs];
-    __shared__ __align__(8) uint64_t sc_full[kSlots], sc_empty[kSlots], fin;
-    __shared__ __align__(16) float s_scale[kSlots][kGroup][NB];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[BUFS], acc_empty[BUFS], fin;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_scan[2 * kThreads / 32];
-    unsigned char* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    LiveExpert* tab = reinterpret_cast<LiveExpert*>(ring + (size_t)a.stages * STAGE);
+    __shared__ volatile long long s_issued[2];
+    __shared__ int s_abort;
+    __shared__ long long s_scan[kThreads / 32];
+    unsigned char* ring = smem_raw;
+    PlanExpert* tab = reinterpret_cast<PlanExpert*>(ring + (size_t)a.stages * STAGE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort_v = &s_abort;
     int* err = &g_gemm8_error;
 
+    if (smem_u32(ring) & 1023) {   // the swizzle counts on it; static shared memory is padded so
+        if (tid == 0) atomicCAS(err, 0, (int)MOE_ERR_UNSUPPORTED);
+        return;
+    }
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < a.stages; i++) {
-            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&full[i]), 2);   // both copy warps
             mbar_init(smem_u32(&empty[i]), 1);
         }
-        for (int i = 0; i < kBufs; i++) {
+        for (int i = 0; i < BUFS; i++) {
             mbar_init(smem_u32(&acc_full[i]), 1);
             mbar_init(smem_u32(&acc_empty[i]), kEpi);
-        }
-        for (int i = 0; i < kSlots; i++) {
-            mbar_init(smem_u32(&sc_full[i]), 2);
-            mbar_init(smem_u32(&sc_empty[i]), kEpi);
         }
         mbar_init(smem_u32(&fin), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
-        tma_prefetch(&tm_a);
-        for (int i = 0; i < kRowMaps && a.box << i <= NB; i++) tma_prefetch(&tm_b.m[i]);
+        for (int i = 0; i < kRowMaps && a.box << i <= 128; i++) tma_prefetch(&tm_a.m[i]);
+    } else if (warp == 2) {
+        tma_prefetch(&tm_b);
     }
-    if (warp == 1) tmem_alloc<1>(smem_u32(&s_tmem), TMEM);
+    if (warp == 1) tmem_alloc<1>(smem_u32(&s_tmem), 512);
     fence_before();
-    const int live = build_live(a.offsets, a.E, a.rows, NB, tab, s_scan);
+    const RowBlocks blocks{128};
+    const int live = build_plan(a.offsets, a.E, a.rows, blocks, tab, s_scan);
     fence_after();
     const uint32_t tmem = s_tmem;
-    RowUnits<NB, 1> units(tab, live, a.M);
-    RowUnit v;
+    PlanWalk tiles(tab, live, blocks, (a.M + NF - 1) / NF, blockIdx.x, gridDim.x);
+    PlanTile v;
 
-    if (warp == 0) {
-        // ============ copies
-        int st = 0, withheld = -1;
-        uint32_t ph = 0;
-        long long issued = 0;
-        bool ok = true;
-        if (elect1()) {
-        while (ok && units.next(v)) {
-            const int ub = row_units(v.n, a.box);
-            const uint32_t bytes = kABytes + (uint32_t)(ub * a.box * 128);
-            for (int b = 0; b < a.blocks; b++) {
-                if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
-                const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
-                if (a.withhold && blockIdx.x == 0 && issued == 0) {
-                    withheld = st;   // testing: never filled, so the wait for it runs out
-                } else {
-                    mbar_expect_tx(bar, bytes);
-                    tma_3d(sa, &tm_a, 128 * b, v.m0, v.e, bar);
-                    tma_rows(sb, tm_b, 128 * b, v.r0, ub, a.box, bar);
-                }
-                issued++;
-                if (++st == a.stages) { st = 0; ph ^= 1; }
-            }
-        }
-        // every issued copy lands before the CTA exits
-        for (int i = 0; i < a.stages && i < issued; i++)
-            if (i != withheld) mbar_drain(smem_u32(&full[i]), i < st ? ph : (ph ^ 1), err);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ============ MMAs: one accumulator per block
-        int st = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
-        bool ok = true;
-        if (elect1()) {
-        while (ok && units.next(v)) {
-            const uint32_t id = idesc_e4m3<1>((v.n + 15) & ~15);
-            for (int b = 0; b < a.blocks; b++) {
-                if (!(ok = mbar_wait(smem_u32(&acc_empty[buf]), bph ^ 1, abort_v, a.wait, err))) break;
-                if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
-                fence_after();
-                const uint32_t sa = smem_u32(ring + (size_t)st * STAGE);
-                const uint64_t da = desc_k(sa), db = desc_k(sa + kABytes);
-#pragma unroll
-                for (int k = 0; k < 4; k++) mma_e4m3<1>(tmem + (uint32_t)(buf * NB), da + 2 * k, db + 2 * k, id, k > 0);
-                commit<1>(smem_u32(&empty[st]));
-                commit<1>(smem_u32(&acc_full[buf]));
-                if (++st == a.stages) { st = 0; ph ^= 1; }
-                if (++buf == kBufs) { buf = 0; bph ^= 1; }
-            }
-        }
-        commit<1>(smem_u32(&fin));
-        mbar_drain(smem_u32(&fin), 0, err);
-        }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ============ scales: xs * ws of four blocks by NB rows per slot
-        constexpr int PER = kGroup * NB / 64;
-        const int t = tid - 64, nb = (a.M + 127) / 128;
-        int slot = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok && units.next(v)) {
-            const float* wsp = a.ws + ((int64_t)v.e * nb + v.m0 / 128) * a.blocks;
-            for (int b0 = 0; b0 < a.blocks; b0 += kGroup) {
-                float s[PER];
-#pragma unroll
-                for (int i = 0; i < PER; i++) {
-                    const int at = t + 64 * i, b = b0 + at / NB, c = at % NB;
-                    s[i] = 0.0f;
-                    if (b < a.blocks && c < v.n)
-                        s[i] = __ldg(a.xs + (int64_t)b * a.rows + v.r0 + c) * __ldg(wsp + b);
-                }
-                if (!(ok = mbar_wait_warp(smem_u32(&sc_empty[slot]), ph ^ 1, abort_v, a.wait, err))) break;
-#pragma unroll
-                for (int i = 0; i < PER; i++) (&s_scale[slot][0][0])[t + 64 * i] = s[i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sc_full[slot]));
-                if (++slot == kSlots) { slot = 0; ph ^= 1; }
-            }
-        }
-    } else {
-        // ============ sums: lane quarter warp % 4, columns CW * half on, one feature per thread
-        const int q = warp & 3, half = (warp - 4) >> 2;
-        int slot = 0, buf = 0;
-        uint32_t sph = 0, bph = 0;
-        bool ok = true;
-        while (ok && units.next(v)) {
-            float acc[CW];
-#pragma unroll
-            for (int c = 0; c < CW; c++) acc[c] = 0.0f;
-            const int c0 = CW * half;
-            for (int b = 0; b < a.blocks; b++) {
-                const int g = b % kGroup;
-                if (g == 0 && !(ok = mbar_wait_warp(smem_u32(&sc_full[slot]), sph, abort_v, a.wait, err))) break;
-                if (!(ok = mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort_v, a.wait, err))) break;
-                fence_after();
-                const uint32_t src = tmem + (uint32_t)(buf * NB + c0) + ((uint32_t)(32 * q) << 16);
-#pragma unroll
-                for (int c = 0; c < CW; c += 16) {
-                    if (c0 + c >= v.n) break;
-                    uint32_t d[16];
-                    tmem_ld16(src + c, d);
-                    wait_ld();
-                    const float4* s4 = reinterpret_cast<const float4*>(&s_scale[slot][g][c0 + c]);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float4 s = s4[j];
-                        acc[c + 4 * j] = fmaf(__uint_as_float(d[4 * j]), s.x, acc[c + 4 * j]);
-                        acc[c + 4 * j + 1] = fmaf(__uint_as_float(d[4 * j + 1]), s.y, acc[c + 4 * j + 1]);
-                        acc[c + 4 * j + 2] = fmaf(__uint_as_float(d[4 * j + 2]), s.z, acc[c + 4 * j + 2]);
-                        acc[c + 4 * j + 3] = fmaf(__uint_as_float(d[4 * j + 3]), s.w, acc[c + 4 * j + 3]);
+    if (warp < 4) {
+        if (SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (warp == 0 || warp == 2) {
+            // ============ copies: warp 0 the rows (A), warp 2 the weights (B)
+            const bool is_a = warp == 0;
+            if (elect1()) {
+                int st = 0;
+                uint32_t ph = 0;
+                long long issued = 0;
+                bool ok = true;
+                while (ok && tiles.next(v)) {
+                    const int ua = row_units(v.n, a.box);
+                    const uint32_t bytes = is_a ? (uint32_t)(ua * a.box * 128) : NF * 128;
+                    for (int b = 0; b < a.blocks; b++) {
+                        if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
+                        const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE);
+                        if (!(a.withhold && blockIdx.x == 0 && issued == 0)) {   // testing: never filled, so the wait runs out
+                            mbar_expect_tx(bar, bytes);
+                            if (is_a) tma_rows(sa, tm_a, 128 * b, v.r0, ua, a.box, bar);
+                            else tma_3d(sa + kABytes, &tm_b, 128 * b, v.m * NF, v.e, bar);
+                        }
+                        issued++;
+                        if (++st == a.stages) { st = 0; ph ^= 1; }
                     }
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&acc_empty[buf]));
-                    if (g == kGroup - 1 || b == a.blocks - 1) mbar_arrive(smem_u32(&sc_empty[slot]));
+                s_issued[is_a] = issued;
+            }
+            __syncwarp();
+            drain_copies(full, a.stages, s_issued, is_a, a.withhold && blockIdx.x == 0, err);
+        } else if (warp == 1) {
+            // ============ MMAs: one accumulator per block
+            if (elect1()) {
+                int st = 0, buf = 0;
+                uint32_t ph = 0, bph = 0;
+                bool ok = true;
+                const uint32_t id = idesc_e4m3<1>(NF);
+                while (ok && tiles.next(v)) {
+                    for (int b = 0; b < a.blocks; b++) {
+                        if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
+                        if (!(ok = mbar_wait(smem_u32(&acc_empty[buf]), bph ^ 1, abort_v, a.wait, err))) break;
+                        fence_after();
+                        const uint32_t sa = smem_u32(ring + (size_t)st * STAGE);
+                        const uint64_t da = desc_k(sa), db = desc_k(sa + kABytes);
+    #pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            mma_e4m3<1>(tmem + (uint32_t)(buf * NF), da + 2 * k, db + 2 * k, id, k > 0);
+                        commit<1>(smem_u32(&empty[st]));
+                        commit<1>(smem_u32(&acc_full[buf]));
+                        if (++st == a.stages) { st = 0; ph ^= 1; }
+                        if (++buf == BUFS) { buf = 0; bph ^= 1; }
+                    }
                 }
-                if (++buf == kBufs) { buf = 0; bph ^= 1; }
-                if ((g == kGroup - 1 || b == a.blocks - 1) && ++slot == kSlots) { slot = 0; sph ^= 1; }
+                commit<1>(smem_u32(&fin));   // every MMA completes before tensor memory is released
+                mbar_drain(smem_u32(&fin), 0, err);
+            }
+            __syncwarp();
+        }
+    } else {
+        if (SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        // ============ sums: rows 32 q + lane, columns c0 .. c0 + CW - 1
+        const int q = warp & 3, c0 = CW * ((warp - 4) >> 2), nb = (a.M + 127) / 128;
+        int buf = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        while (ok && tiles.next(v)) {
+            const int m0 = v.m * NF + c0;                      // the warp's first feature
+            const bool works = 32 * q < v.n && m0 < a.M;   // the warp has rows and features
+            const bool mine = works && 32 * q + lane < v.n;
+            const float* xsp = a.xs + v.r0 + 32 * q + lane;
+            const float* wsp = a.ws + ((int64_t)v.e * nb + m0 / 128) * a.blocks;
+            float acc[CW], xs[GROUP], ws[GROUP];
+            auto fetch = [&](int b0) {
+#pragma unroll
+                for (int g = 0; g < GROUP; g++) {
+                    const bool in = mine && b0 + g < a.blocks;
+                    xs[g] = fetch_f32(xsp + (int64_t)(b0 + g) * a.rows, in);
+                    ws[g] = fetch_f32(wsp + b0 + g, in);
+                }
+            };
+#pragma unroll
+            for (int c = 0; c < CW; c++) acc[c] = 0.0f;
+            fetch(0);
+            for (int b0 = 0; ok && b0 < a.blocks; b0 += GROUP) {
+                float s[GROUP];
+#pragma unroll
+                for (int g = 0; g < GROUP; g++) s[g] = xs[g] * ws[g];
+                fetch(b0 + GROUP);
+#pragma unroll
+                for (int g = 0; g < GROUP; g++) {
+                    if (b0 + g >= a.blocks) break;
+                    if (!(ok = mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort_v, a.wait, err))) break;
+                    fence_after();
+                    if (works) {
+                        const uint32_t src = tmem + (uint32_t)(buf * NF + c0) + ((uint32_t)(32 * q) << 16);
+                        uint32_t d[2][16];   // 16 columns on their way while 16 are added
+                        tmem_ld16(src, d[0]);
+#pragma unroll
+                        for (int c = 0; c < CW; c += 16) {
+                            wait_ld(d[(c / 16) & 1]);
+                            if (c + 16 < CW) tmem_ld16(src + c + 16, d[(c / 16 + 1) & 1]);
+#pragma unroll
+                            for (int j = 0; j < 16; j++)
+                                acc[c + j] = fmaf(__uint_as_float(d[(c / 16) & 1][j]), s[g], acc[c + j]);
+                        }
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+                    if (++buf == BUFS) { buf = 0; bph ^= 1; }
+                }
             }
             if (!ok) break;
-            const int f = v.m0 + 32 * q + lane;
-            if (f < a.M) {
-                const int64_t at = (int64_t)(v.r0 + c0) * a.ldo + f;
-                float* of = static_cast<float*>(a.out) + at;
-                uint16_t* oh = static_cast<uint16_t*>(a.out) + at;
+            if (mine) {
+                const int64_t at = (int64_t)(v.r0 + 32 * q + lane) * a.ldo + m0;
+                const int n = min(CW, a.M - m0);   // a multiple of 8
+                if (a.out_f32) {
+                    float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
-                for (int c = 0; c < CW; c++) {
-                    if (c0 + c >= v.n) break;
-                    if (a.out_f32) of[c * a.ldo] = acc[c];
-                    else oh[c * a.ldo] = f32_to_bf16_bits(acc[c]);
+                    for (int c = 0; c < CW; c += 8)
+                        if (c < n) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; j++) w[j] = __float_as_uint(acc[c + j]);
+                            store32(o + c, w, a.wide);
+                        }
+                } else {
+                    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+                    for (int c = 0; c < CW; c += 16)
+                        if (c < n) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; j++) w[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
+                            if (c + 8 < n) store32(o + c, w, a.wide);
+                            else *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                 }
             }
             __syncwarp();
@@ -242,27 +287,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         fence_after();
-        tmem_dealloc<1>(tmem, TMEM);
+        tmem_dealloc<1>(tmem, 512);
     }
 }
 
-template <int NB>
-int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, cudaStream_t st)
+template <int NF>
+int launch(Args& a, const RowMaps& ta, const CUtensorMap& tb, cudaStream_t st)
 {
-    constexpr int STAGE = kABytes + NB * 128;
+    constexpr int STAGE = kABytes + NF * 128;
     int sms = 0;
     if (int rc = device_sms(&sms)) return rc;
-    const int table = (int)align_up(sizeof(LiveExpert) * (a.E + 1), 128);
-    const int fixed = kSlots * kGroup * NB * 4 + 1024;   // scale ring, barriers
-    a.stages = (kSmemMax - fixed - 1024 - table) / STAGE;
+    const int fixed = plan_bytes(a.E);
+    a.stages = (kSmemMax - 1024 - fixed) / STAGE;   // 1 KB static
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    const int smem = 1024 + a.stages * STAGE + table;
-    auto* kern = gg8_kernel<NB>;
+    const int smem = fixed + a.stages * STAGE;
+    auto* kern = gg8_kernel<NF>;
+    if (NF == 256) {   // the register split counts on what the kernel was compiled to
+        static const int regs = [] {
+            cudaFuncAttributes at{};
+            return cudaFuncGetAttributes(&at, gg8_kernel<NF>) == cudaSuccess ? at.numRegs : 0;
+        }();
+        if (regs != kRegs) return MOE_ERR_UNSUPPORTED;
+    }
     MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    kern<<<sms, kThreads, smem, st>>>(ta, tb, a);
-    MOE_LAUNCH_CHECK();
+    MOE_CUDA_TRY(launch_clusters(kern, sms, 1, kThreads, smem, st, ta, tb, a));
     return MOE_OK;
 }
 
@@ -301,22 +351,24 @@ extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, co
     a.out = d_y;
     a.ldo = ldy;
     a.out_f32 = y_dtype == MOE_DT_F32;
+    a.wide = !(((uintptr_t)d_y | (uintptr_t)(ldy * dtype_size(y_dtype))) & 31);
     a.E = experts;
     a.rows = rows;
     a.M = out;
     a.blocks = (in + 127) / 128;
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
-    const bool small = rows <= 16 * (int64_t)experts;
-    a.box = small ? 16 : 32;
-    CUtensorMap ta;
-    RowMaps tb;
+    // 128 features a tile while the call streams weights for few rows: more
+    // tiles to spread over the SMs
+    const bool few = rows <= 16 * (int64_t)experts;
+    a.box = few ? 16 : 32;
+    RowMaps ta;
+    CUtensorMap tb;
     const uint64_t wd[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)experts};
     const uint64_t wst[2] = {(uint64_t)in, (uint64_t)in * out};
-    const uint32_t wb[3] = {128, 128, 1};
-    if (!encode_map(&ta, E_U8, 3, d_wq, wd, wst, wb) ||
-        !encode_rows(&tb, E_U8, d_xq, ldxq, in, rows, a.box, small ? 32 : 128))
+    const uint32_t wb[3] = {128, few ? 128u : 256u, 1};
+    if (!encode_rows(&ta, E_U8, d_xq, ldxq, in, rows, a.box, 128) || !encode_map(&tb, E_U8, 3, d_wq, wd, wst, wb))
         return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return small ? launch_nb<32>(a, ta, tb, st) : launch_nb<128>(a, ta, tb, st);
+    return few ? launch<128>(a, ta, tb, st) : launch<256>(a, ta, tb, st);
 }

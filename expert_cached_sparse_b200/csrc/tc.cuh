@@ -43,13 +43,14 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// One arrival by the calling lane on a barrier anywhere in the cluster.  What
-// it announces was written by the async proxy (copies) or read from tensor
-// memory; a release at cluster scope, which waits for every earlier store of
-// the thread, is left to callers with writes of their own to publish.
+// One arrival by the calling lane on a barrier anywhere in the cluster, with
+// no ordering of the thread's own writes (a release there is a memory barrier
+// of about a thousand cycles).  What it announces is already in place: copies
+// whose completion the thread has seen, accumulators read.  Callers with
+// writes of their own to publish fence first.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------ mbarriers
@@ -155,10 +156,26 @@ template <int N>   // all but the newest N groups have read their source
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// End of the two copy warps of a CTA (converged, `is_a` one of them): every
+// issued copy lands before the CTA exits.  After an abort one warp may be
+// ahead; the other arrives for the stages it did not fill, so that their
+// phases complete with the copies in flight.  `withheld`: the CTA's first
+// stage never completes (a test's doing).
+__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, volatile long long* issued, bool is_a,
+                                             bool withheld, int* error)
+{
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    const long long mine = issued[is_a], most = max(mine, issued[!is_a]);
+    if ((threadIdx.x & 31) == 0)
+        for (long long i = mine; i < most; i++) mbar_arrive(smem_u32(&full[i % stages]));
+    if (is_a)
+        for (long long i = most > stages ? most - stages : 0; i < most; i++)
+            if (i > 0 || !withheld) mbar_drain(smem_u32(&full[i % stages]), (uint32_t)(i / stages) & 1, error);
+}
+
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // One arrival on `bar` once every MMA issued so far has finished; for a pair
 // (CG = 2) on the barrier at that address in both CTAs.
 template <int CG>
@@ -242,7 +259,9 @@ MOE_TC_MMA(mma_bf16, "f16")
 MOE_TC_MMA(mma_e4m3, "f8f6f4")
 #undef MOE_TC_MMA
 
-// 16 consecutive columns of the warp's 32 lanes (32 * (warp % 4) on).
+// 16 consecutive columns of the warp's 32 lanes (32 * (warp % 4) on).  The
+// registers hold them only after wait_ld, which takes the registers through
+// itself so that no use is moved ahead of it.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
@@ -252,6 +271,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v)
                    "=r"(v[15])
                  : "r"(addr)
                  : "memory");
+}
+__device__ __forceinline__ void hold16(uint32_t* v)
+{
+    asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                      "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                      "+r"(v[15]));
+}
+__device__ __forceinline__ void wait_ld(uint32_t* v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    hold16(v);
 }
 
 // ------------------------------------------------------------------ host: tensor maps
@@ -292,104 +322,154 @@ bool encode_rows(RowMaps* r, Elem type, const void* p, int64_t ld, int width, in
 
 }  // namespace tc
 
-// ------------------------------------------------------------------ units of the row-grouped products
-// One live expert: the token blocks before its first one, its id and rows.
-struct LiveExpert {
-    int pre, e, r0, r1;
+// ------------------------------------------------------------------ the plan of a call
+// A call's tiles run through its experts, an expert's feature tiles, and
+// fastest the blocks of rows of a feature tile.  CTA (or pair) c takes tiles c, c + G, c + 2 G, ... of G,
+// so that what runs at one time is neighbours, which share weights and rows in
+// L2 (equal contiguous runs of tiles, one a CTA, took 1.4 to 1.8 times as
+// long on 4096 tokens: each expert's rows were read again for every feature
+// tile; the largest experts first, for even rounds, took up to 1.25 times as
+// long: tiles bound by their weights no longer ran beside those bound by MMAs).
+struct PlanExpert {
+    int pre;       // blocks of the experts before
+    int e, r0, r1; // expert and its rows
 };
 
-// The call's live experts in ascending order, in shared memory, with one
-// closing entry {total token blocks}; NB rows per token block.  Called by all
-// threads of the CTA; `scratch` holds 2 ints per warp.  Returns how many.
-// Ranges that no offsets of moe_permute would hold count as empty; ranges
-// that overlap so often that the blocks pass 2^31 void the whole call.
-__device__ __forceinline__ int build_live(const int32_t* __restrict__ offsets, int E, int rows, int NB,
-                                          LiveExpert* tab, int* scratch)
+// How an expert's rows are cut into blocks.
+struct RowBlocks {
+    int size;   // most rows of a block, a multiple of 32
+    __device__ __forceinline__ int blocks(int rows) const { return (rows + size - 1) / size; }
+    // rows of a block: equal shares, in 32s
+    __device__ __forceinline__ int share(int rows) const
+    {
+        const int n = blocks(rows);
+        return n == 1 ? size : ((rows + n - 1) / n + 31) & ~31;
+    }
+};
+
+// Rows of expert e; none for a range that no offsets of moe_permute hold.
+__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int rows, int& lo, int& hi)
+{
+    lo = __ldg(offsets + e);
+    hi = __ldg(offsets + e + 1);
+    if (lo < 0 || hi < lo || hi > rows) lo = hi = 0;
+}
+
+// Bytes of a plan's table in shared memory.
+__host__ __device__ static inline int plan_bytes(int E) { return (int)align_up(sizeof(PlanExpert) * (E + 1), 128); }
+
+// Builds the table in shared memory: the experts with rows in ascending order,
+// then a closing entry {blocks in all}.  Called by all threads; returns the
+// number of experts.  Ranges that overlap so often that the blocks pass 2^31
+// void the call.
+__device__ __forceinline__ int build_plan(const int32_t* __restrict__ offsets, int E, int rows, const RowBlocks& B,
+                                          PlanExpert* tab, long long* scratch)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-    const int per = (E + nt - 1) / nt;
-    const int e0 = tid * per, e1 = min(E, e0 + per);
-    int n = 0;
-    long long b = 0;
+    const int per = (E + nt - 1) / nt, e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    // experts in the low 13 bits, blocks above: one sum for both
+    long long sum = 0;
     for (int e = e0; e < e1; e++) {
-        const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
-        if (lo >= 0 && hi > lo && hi <= rows) {
-            n++;
-            b += (hi - lo + NB - 1) / NB;
-        }
+        int lo, hi;
+        expert_rows(offsets, e, rows, lo, hi);
+        if (hi > lo) sum += ((long long)B.blocks(hi - lo) << 13) + 1;
     }
-    int ni = n;
-    long long bi = b;
+    long long in = sum;
     for (int o = 1; o < 32; o <<= 1) {
-        const int nn = __shfl_up_sync(0xffffffffu, ni, o);
-        const long long bb = __shfl_up_sync(0xffffffffu, bi, o);
-        if (lane >= o) { ni += nn; bi += bb; }
+        const long long x = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += x;
     }
-    if (lane == 31) {
-        scratch[2 * warp] = ni;
-        scratch[2 * warp + 1] = (int)min(bi, (long long)0x7fffffff);
-    }
+    if (lane == 31) scratch[warp] = in;
     __syncthreads();
-    int live = 0, nb = ni - n;
-    long long total = 0, base = bi - b;
+    long long base = in - sum, total = 0;
     for (int w = 0; w < nt / 32; w++) {
-        if (w < warp) { nb += scratch[2 * w]; base += scratch[2 * w + 1]; }
-        live += scratch[2 * w];
-        total += scratch[2 * w + 1];
+        if (w < warp) base += scratch[w];
+        total += scratch[w];
     }
-    if (total >= 0x7fffffff) live = 0;
-    else
+    const bool voided = total >> 13 > 0x7fffffff;
+    const int live = voided ? 0 : (int)(total & 8191);
+    if (!voided)
         for (int e = e0; e < e1; e++) {
-            const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
-            if (lo >= 0 && hi > lo && hi <= rows) {
-                tab[nb++] = {(int)base, e, lo, hi};
-                base += (hi - lo + NB - 1) / NB;
-            }
+            int lo, hi;
+            expert_rows(offsets, e, rows, lo, hi);
+            if (hi == lo) continue;
+            tab[base & 8191] = {(int)(base >> 13), e, lo, hi};
+            base += ((long long)B.blocks(hi - lo) << 13) + 1;
         }
-    if (tid == 0) tab[live] = {live ? (int)total : 0, 0, 0, 0};
+    if (tid == 0) tab[live] = {voided ? 0 : (int)(total >> 13), 0, 0, 0};
     __syncthreads();
     return live;
 }
 
-// A tile of the row products: 128 features (256 for a pair of CTAs) from m0
-// on, n rows from r0 on, of expert e's matrix.
-struct RowUnit {
-    int e, m0, r0, n;
+// A tile: the m-th feature tile of expert e, n rows from r0 on.
+struct PlanTile {
+    int e, m, r0, n;
 };
 
-// The tiles of a CTA or pair: u = its number, then every grid's worth on.  An
-// expert's token blocks run fastest, then its feature tiles, so that CTAs
-// running together share weight tiles and rows in L2.
-template <int NB, int CG>
-struct RowUnits {
-    const LiveExpert* tab;
-    int live, mt;
+// Walks a CTA's tiles: number `part` of `parts`, mt feature tiles an expert.
+struct PlanWalk {
+    const PlanExpert* tab;
+    const RowBlocks B;
+    int live, mt, i, parts;
     long long u, total;
 
-    __device__ RowUnits(const LiveExpert* t, int live_, int M)
-        : tab(t), live(live_), mt((M + 128 * CG - 1) / (128 * CG)), u(blockIdx.x / CG), total((long long)t[live_].pre * mt)
+    __device__ PlanWalk(const PlanExpert* t, int live_, const RowBlocks& b, int mt_, int part, int parts_)
+        : tab(t), B(b), live(live_), mt(mt_), i(0), parts(parts_), u(part), total((long long)t[live_].pre * mt_)
     {
     }
-    __device__ bool next(RowUnit& v)
+    __device__ __forceinline__ bool next(PlanTile& v)
     {
         if (u >= total) return false;
-        int lo = 0, hi = live - 1;   // the last live expert whose first tile is at most u
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((long long)tab[mid].pre * mt <= u) lo = mid;
+        int hi = min(live - 1, i + parts);   // every expert has a tile at least
+        while (i < hi) {                     // the last expert whose first tile is at most u
+            const int mid = (i + hi + 1) >> 1;
+            if ((long long)tab[mid].pre * mt <= u) i = mid;
             else hi = mid - 1;
         }
-        const LiveExpert L = tab[lo];
-        const long long r = u - (long long)L.pre * mt;
-        const int nt = (L.r1 - L.r0 + NB - 1) / NB;
-        v.e = L.e;
-        v.m0 = (int)(r / nt) * (128 * CG);
-        v.r0 = L.r0 + (int)(r % nt) * NB;
-        v.n = min(NB, L.r1 - v.r0);
-        u += gridDim.x / CG;
+        const PlanExpert x = tab[i];
+        const long long r = u - (long long)x.pre * mt;
+        const int nt = B.blocks(x.r1 - x.r0);
+        int m, t = 0;
+        if (nt == 1) m = (int)r;
+        else if (r < 0x7fffffff) {   // a 64-bit division takes hundreds of cycles
+            m = (int)r / nt;
+            t = (int)r - m * nt;
+        } else {
+            m = (int)(r / nt);
+            t = (int)(r % nt);
+        }
+        const int share = B.share(x.r1 - x.r0), r0 = x.r0 + t * share;
+        v = {x.e, m, r0, min(share, x.r1 - r0)};
+        u += parts;
         return true;
     }
 };
+
+// Rows that the MMAs of a tile of n rows take: a multiple of 16 for each CTA.
+template <int CG>
+__device__ __forceinline__ int mma_rows(int n)
+{
+    return (n + 16 * CG - 1) / (16 * CG) * (16 * CG);
+}
+
+// One CTA, or one cluster of CG, per SM or CG of them.
+template <class... P, class... A>
+static inline cudaError_t launch_clusters(void (*kern)(P...), int sms, int CG, int threads, int smem, cudaStream_t st,
+                                          const A&... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms / CG * CG);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 // ------------------------------------------------------------------ host: checks common to the products
 constexpr int64_t kMaxGemmDim = 1 << 20;

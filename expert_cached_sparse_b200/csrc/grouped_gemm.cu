@@ -48,6 +48,13 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
 constexpr int kStaging = 4 * 2 * 4096;
 
+// Steps of 64 summed in one accumulator where the output is float32.  The
+// tensor core adds to its fp32 accumulator with truncation, so the relative
+// error of a sum grows by about 1e-6 for every 1000 inner indices; partial
+// sums of 512 are added to the output, rounded to nearest.  (bf16 outputs
+// round to 2^-9 anyway: one accumulator for the whole sum.)
+constexpr int kPartial = 8;
+
 enum Mode { FWD, DX, DW };
 
 struct Args {
@@ -60,6 +67,7 @@ struct Args {
     int M, N;        // features; DW: columns (`in`)
     int K;           // inner size (DW: ragged)
     int stages;
+    int partial;     // steps summed in one accumulator
     int box;         // smallest height of a copy of the ragged operand (FWD, DX)
     int chunks_a, chunks_b;   // whether one copy brings all 64-column chunks of an MN-major operand
     long long wait;  // limit of every bounded wait, in SM clock cycles
@@ -138,13 +146,17 @@ struct Units<DW, NB, 1> {
     }
 };
 
-__device__ __forceinline__ void put(float* p, uint32_t d) { *p = __uint_as_float(d); }
-__device__ __forceinline__ void put(uint16_t* p, uint32_t d) { *p = f32_to_bf16_bits(__uint_as_float(d)); }
+__device__ __forceinline__ void put(float* p, uint32_t d, bool add)
+{
+    const float x = __uint_as_float(d);
+    *p = add ? *p + x : x;
+}
+__device__ __forceinline__ void put(uint16_t* p, uint32_t d, bool) { *p = f32_to_bf16_bits(__uint_as_float(d)); }
 
 // A warp's 32 features of n columns, ldo elements apart: each store is 32
 // adjacent elements of one column.  `mine`: whether the lane's feature exists.
 template <class T>
-__device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int n, bool mine)
+__device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int n, bool mine, bool add)
 {
     for (int c = 0; c < n; c += 16) {
         uint32_t d[16];
@@ -153,7 +165,7 @@ __device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int 
         if (mine) {
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-                if (c + j < n) put(p, d[j]);
+                if (c + j < n) put(p, d[j], add);
                 p += ldo;
             }
         }
@@ -188,6 +200,51 @@ __device__ __forceinline__ void add_row16(uint16_t* p, const uint32_t (&d)[16], 
     }
 }
 
+// A warp's 32 rows of dW from row r0 on go out by TMA, 128 bytes of each at a
+// time, through two swizzled tiles in shared memory; zeros where `none`.
+__device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap& out, const Unit& v, unsigned char* tiles,
+                                           int& turn, uint32_t src, int r0, bool none, bool add)
+{
+    const int lane = threadIdx.x & 31, w = a.out_f32 ? 32 : 64;
+    for (int c = 0; c < v.n; c += w, turn ^= 1) {
+        unsigned char* tile = tiles + 4096 * turn;
+        if (lane == 0) bulk_wait_read<1>();   // its previous rows are on their way
+        __syncwarp();
+        for (int h = 0; h < w / 32; h++) {
+            uint32_t d[32];
+            if (none) {
+#pragma unroll
+                for (int j = 0; j < 32; j++) d[j] = 0;
+            } else {
+                tmem_ld16(src + c + 32 * h, d);
+                tmem_ld16(src + c + 32 * h + 16, d + 16);
+                wait_ld(d);
+                hold16(d + 16);
+            }
+            unsigned char* row = tile + 128 * lane;
+            if (a.out_f32) {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    *reinterpret_cast<uint4*>(row + 16 * (j ^ (lane & 7))) =
+                        make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    *reinterpret_cast<uint4*>(row + 16 * ((j + 4 * h) ^ (lane & 7))) =
+                        make_uint4(pack_bf16(d[8 * j], d[8 * j + 1]), pack_bf16(d[8 * j + 2], d[8 * j + 3]),
+                                   pack_bf16(d[8 * j + 4], d[8 * j + 5]), pack_bf16(d[8 * j + 6], d[8 * j + 7]));
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tma_add_3d(&out, smem_u32(tile), v.c0 + c, r0, v.e);
+            else tma_store_3d(&out, smem_u32(tile), v.c0 + c, r0, v.e);
+            bulk_commit();
+        }
+    }
+}
+
 template <int MODE, int NB, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
@@ -200,9 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
     __shared__ uint32_t s_tmem;
-    __shared__ volatile long long s_issued[2];
-    __shared__ int s_abort;
-    __shared__ long long s_scan[kThreads / 32];
+    __shared__ CopyPos s_copy[2];
+    __shared__ int s_abort, s_live;
+    __shared__ long long s_scan[4];
     unsigned char* ring = smem_raw;
     unsigned char* staging = ring + (size_t)a.stages * STAGE;   // DW: 4 warps x 2 tiles of 32 rows x 128 bytes
     PlanExpert* tab = reinterpret_cast<PlanExpert*>(staging + (MODE == DW ? kStaging : 0));
@@ -232,77 +289,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) {
         tma_prefetch(&tm_a);
+    } else if (warp == 1) {
+        tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);
     } else if (warp == 2) {
         for (int i = 0; i < kRowMaps && a.box << i <= NB / CG; i++) tma_prefetch(&tm_b.m[i]);
+    } else if (warp >= 4) {
+        if constexpr (MODE == DW)
+            for (int i = tid - 128; i <= a.E; i += 128) off[i] = __ldg(a.offsets + i);
+        else
+            build_plan<128>(a.offsets, a.E, a.rows, {NB}, tab, s_scan, &s_live);
     }
-    if (warp == 1) tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);
     fence_before();
-    int live = 0;
-    if (MODE == DW) {
-        for (int i = tid; i <= a.E; i += kThreads) off[i] = __ldg(a.offsets + i);
-        __syncthreads();
-    } else {
-        live = build_plan(a.offsets, a.E, a.rows, {NB}, tab, s_scan);
-    }
+    __syncthreads();
     if (PAIR) cluster_sync();   // the peer's barriers exist
     fence_after();
     const uint32_t tmem = s_tmem;
-    Units<MODE, NB, CG> units(a, tab, off, live, rank);
+    Units<MODE, NB, CG> units(a, tab, off, MODE == DW ? 0 : s_live, rank);
     Unit v;
 
-    if (warp == 0 || warp == 2) {
-        // ============ copies: warp 0 the features (A), warp 2 the columns (B)
-        const bool is_a = warp == 0;
+    if (warp == 0) {
+        // ============ copies of the features (A)
+        if (elect1())
+            copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
+                             [&] { return units.next(v) ? v.steps : -1; },
+                             [&](int s, uint32_t bar, uint32_t sa) {
+                                 const int k = v.k0 + 64 * s;
+                                 mbar_expect_tx(bar, kABytes);
+                                 if (MODE == FWD) {
+                                     tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
+                                 } else if (a.chunks_a) {
+                                     if (MODE == DX) tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
+                                     else tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
+                                 } else
+                                     for (int i = 0; i < 2; i++) {
+                                         if (MODE == DX) tma_3d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, v.e, bar);
+                                         else tma_2d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, bar);
+                                     }
+                             });
+        __syncwarp();
+        drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
+    } else if (warp == 2) {
+        // ============ copies of the columns (B)
         if (elect1()) {
-            int st = 0;
-            uint32_t ph = 0;
-            long long issued = 0;
-            bool ok = true;
-            while (ok && units.next(v)) {
-                const int ub = MODE == DW ? (a.chunks_b ? NB / CG / 64 : (v.nh + 63) / 64) : row_units(v.nb, a.box);
-                const uint32_t bytes = is_a ? kABytes : (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
-                for (int s = 0; s < v.steps; s++) {
-                    if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
-                    const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
-                    const int k = v.k0 + 64 * s;
-                    if (a.withhold && blockIdx.x == 0 && issued == 0) {
-                        // testing: never filled, so the wait for it runs out
-                    } else if (is_a) {
-                        mbar_expect_tx(bar, bytes);
-                        if (MODE == FWD) {
-                            tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
-                        } else if (MODE == DX) {
-                            if (a.chunks_a) {
-                                tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
-                            } else {
-                                tma_3d(sa, &tm_a, v.m0, k, v.e, bar);
-                                tma_3d(sa + 8192, &tm_a, v.m0 + 64, k, v.e, bar);
-                            }
-                        } else if (a.chunks_a) {
-                            tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
-                        } else {
-                            tma_2d(sa, &tm_a, v.m0, k, bar);
-                            tma_2d(sa + 8192, &tm_a, v.m0 + 64, k, bar);
-                        }
-                    } else if (bytes == 0) {
-                        mbar_arrive(bar);   // a pair's second half without columns
-                    } else {
-                        mbar_expect_tx(bar, bytes);
-                        if (MODE != DW)
-                            tma_rows(sb, tm_b, k, v.cb, ub, a.box, bar);
-                        else if (a.chunks_b)
-                            tma_3d(sb, &tm_b.m[0], 0, k, v.cb / 64, bar);
-                        else
-                            for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.cb + 64 * i, k, bar);
-                    }
-                    issued++;
-                    if (++st == a.stages) { st = 0; ph ^= 1; }
-                }
-            }
-            s_issued[is_a] = issued;
+            int ub = 0;
+            uint32_t bytes = 0;
+            copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
+                             [&] {
+                                 if (!units.next(v)) return -1;
+                                 ub = MODE == DW ? (a.chunks_b ? NB / 64 : (v.n + 63) / 64) : row_units(v.nb, a.box);
+                                 bytes = (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
+                                 return v.steps;
+                             },
+                             [&](int s, uint32_t bar, uint32_t sa) {
+                                 const int k = v.k0 + 64 * s;
+                                 const uint32_t sb = sa + kABytes;
+                                 if (PAIR && bytes == 0) {   // a pair's second half without columns
+                                     mbar_arrive(bar);
+                                     return;
+                                 }
+                                 mbar_expect_tx(bar, bytes);
+                                 if (MODE != DW)
+                                     tma_rows(sb, tm_b, k, v.cb, ub, a.box, bar);
+                                 else if (a.chunks_b)
+                                     tma_3d(sb, &tm_b.m[0], 0, k, v.cb / 64, bar);
+                                 else
+                                     for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.cb + 64 * i, k, bar);
+                             });
         }
         __syncwarp();
-        drain_copies(full, a.stages, s_issued, is_a, a.withhold && blockIdx.x == 0, err);
+        drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
     } else if (warp == 1) {
         // ============ MMAs
         if (rank == 0) {
@@ -311,16 +366,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t ph = 0;
                 bool ok = true;
                 while (ok && units.next(v)) {
-                    if (v.steps == 0) continue;   // DW: an expert without rows
-                    const int ab = it & 1;
-                    if (it >= 2) {   // the epilogue has read this accumulator's previous unit
-                        if (!(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
-                            break;
-                        fence_after();
-                    }
-                    const uint32_t d = tmem + (uint32_t)(ab * NB);
                     const uint32_t id = idesc_bf16<CG>(CG * v.nh, MODE != FWD, MODE == DW);
+                    uint32_t d = 0;
+                    int left = 0;   // steps until the accumulator changes
                     for (int s = 0; s < v.steps; s++) {
+                        const bool first = left == 0;
+                        if (first) {
+                            const int ab = it & 1;
+                            if (it >= 2 &&   // the epilogue has read what this accumulator held
+                                !(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
+                                break;
+                            d = tmem + (uint32_t)(ab * NB);
+                            left = min(a.partial, v.steps - s);
+                        }
                         const uint32_t bar = smem_u32(RELAY ? &ready[st] : &full[st]);
                         if (!(ok = mbar_wait(bar, ph, abort_v, a.wait, err))) break;
                         fence_after();
@@ -333,13 +391,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; k++)
                             if (MODE != DW || k < kk)
                                 mma_bf16<CG>(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id,
-                                             s > 0 || k > 0);
+                                             !first || k > 0);
                         commit<CG>(smem_u32(&empty[st]));   // the stage is free once these MMAs have read it
                         if (++st == a.stages) { st = 0; ph ^= 1; }
+                        if (--left == 0) {
+                            commit<CG>(smem_u32(&acc_full[it & 1]));
+                            it++;
+                        }
                     }
-                    if (!ok) break;
-                    commit<CG>(smem_u32(&acc_full[ab]));
-                    it++;
                 }
                 commit<CG>(smem_u32(&fin));   // every MMA completes before tensor memory is released
                 mbar_drain(smem_u32(&fin), 0, err);
@@ -380,81 +439,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0, turn = 0;
         bool ok = true;
         while (ok && units.next(v)) {
-            const int f = v.m0 + 32 * q + lane, ab = it & 1;
+            const int f = v.m0 + 32 * q + lane;
+            const bool mine = f < a.M;
             const bool none = MODE == DW && v.steps == 0;   // an expert without rows: its gradient is zero
             if (none && a.accumulate) continue;
-            if (!none) {
-                if (!(ok = mbar_wait_warp(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
-                fence_after();
-            }
-            const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
-            const bool mine = f < a.M;
-            if (MODE == DW && a.direct) {
-                // a thread's feature is a row of dW: 16 adjacent columns at a time
-                const int64_t at = ((int64_t)v.e * a.M + f) * a.N + v.c0;
-                for (int c = 0; c < v.n; c += 16) {
-                    uint32_t d[16];
-                    tmem_ld16(src + c, d);
-                    wait_ld(d);
-                    if (mine) add_row16(static_cast<uint16_t*>(a.out) + at + c, d, v.n - c);
-                    __syncwarp();   // the warp's next tensor-memory load is a converged one
+            // one accumulator, or the partial sums of every a.partial steps
+            for (int s = 0; s == 0 || s < v.steps; s += a.partial) {
+                const int ab = it & 1;
+                const bool add = s > 0 || (MODE == DW && a.accumulate);   // to what is there
+                if (!none) {
+                    if (!(ok = mbar_wait_warp(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+                    fence_after();
                 }
-            } else if (MODE == DW) {
-                // a warp's 32 rows of dW go out by TMA, 128 bytes of each at a time, through
-                // two swizzled tiles in shared memory (zeros for an expert without rows)
-                const int w = a.out_f32 ? 32 : 64;
-                if (v.m0 + 32 * q < a.M)
-                    for (int c = 0; c < v.n; c += w, turn ^= 1) {
-                        unsigned char* tile = staging + 8192 * q + 4096 * turn;
-                        if (lane == 0) bulk_wait_read<1>();   // its previous rows are on their way
-                        __syncwarp();
-                        for (int h = 0; h < w / 32; h++) {
-                            uint32_t d[32];
-                            if (none) {
-#pragma unroll
-                                for (int j = 0; j < 32; j++) d[j] = 0;
-                            } else {
-                                tmem_ld16(src + c + 32 * h, d);
-                                tmem_ld16(src + c + 32 * h + 16, d + 16);
-                                wait_ld(d);
-                                hold16(d + 16);
-                            }
-                            unsigned char* row = tile + 128 * lane;
-                            if (a.out_f32) {
-#pragma unroll
-                                for (int j = 0; j < 8; j++)
-                                    *reinterpret_cast<uint4*>(row + 16 * (j ^ (lane & 7))) =
-                                        make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 4; j++)
-                                    *reinterpret_cast<uint4*>(row + 16 * ((j + 4 * h) ^ (lane & 7))) =
-                                        make_uint4(pack_bf16(d[8 * j], d[8 * j + 1]), pack_bf16(d[8 * j + 2], d[8 * j + 3]),
-                                                   pack_bf16(d[8 * j + 4], d[8 * j + 5]),
-                                                   pack_bf16(d[8 * j + 6], d[8 * j + 7]));
-                            }
+                const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
+                if constexpr (MODE == DW) {
+                    if (a.direct) {
+                        // a thread's feature is a row of dW: 16 adjacent columns at a time
+                        const int64_t at = ((int64_t)v.e * a.M + f) * a.N + v.c0;
+                        for (int c = 0; c < v.n; c += 16) {
+                            uint32_t d[16];
+                            tmem_ld16(src + c, d);
+                            wait_ld(d);
+                            if (mine) add_row16(static_cast<uint16_t*>(a.out) + at + c, d, v.n - c);
+                            __syncwarp();   // the warp's next tensor-memory load is a converged one
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (a.accumulate) tma_add_3d(&tm_out, smem_u32(tile), v.c0 + c, v.m0 + 32 * q, v.e);
-                            else tma_store_3d(&tm_out, smem_u32(tile), v.c0 + c, v.m0 + 32 * q, v.e);
-                            bulk_commit();
-                        }
+                    } else if (v.m0 + 32 * q < a.M) {
+                        if (s > 0 && lane == 0) bulk_wait();   // the partial sums before are in place
+                        store_tile(a, tm_out, v, staging + 8192 * q, turn, src, v.m0 + 32 * q, none, add);
                     }
-                if (none) continue;
-            } else if (a.out_f32) {
-                store_cols(static_cast<float*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
-            } else {
-                store_cols(static_cast<uint16_t*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
+                } else if (a.out_f32) {
+                    store_cols(static_cast<float*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine, add);
+                } else {
+                    store_cols(static_cast<uint16_t*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine, false);
+                }
+                if (none) break;
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&acc_empty[ab]), 0));
+                    else mbar_arrive(smem_u32(&acc_empty[ab]));
+                }
+                it++;
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&acc_empty[ab]), 0));
-                else mbar_arrive(smem_u32(&acc_empty[ab]));
-            }
-            it++;
         }
         if (MODE == DW && lane == 0) bulk_wait();   // the staging tiles are read, the stores done
     }
@@ -515,6 +541,7 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     a.out = y;
     a.ldo = ldy;
     a.out_f32 = y_dtype == MOE_DT_F32;
+    a.partial = a.out_f32 ? kPartial : 1 << 30;
     a.E = E;
     a.rows = rows;
     a.M = MODE == FWD ? out : in;
@@ -636,6 +663,7 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     a.ldo = in;
     a.out_f32 = dw_dtype == MOE_DT_F32;
     a.accumulate = accumulate ? 1 : 0;
+    a.partial = a.out_f32 ? kPartial : 1 << 30;
     a.E = experts;
     a.rows = rows;
     a.M = out;

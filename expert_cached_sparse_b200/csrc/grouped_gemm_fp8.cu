@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[BUFS], acc_empty[BUFS], fin;
     __shared__ uint32_t s_tmem;
-    __shared__ volatile long long s_issued[2];
-    __shared__ int s_abort;
-    __shared__ long long s_scan[kThreads / 32];
+    __shared__ CopyPos s_copy[2];
+    __shared__ int s_abort, s_live;
+    __shared__ long long s_scan[kEpi];
     unsigned char* ring = smem_raw;
     PlanExpert* tab = reinterpret_cast<PlanExpert*>(ring + (size_t)a.stages * STAGE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -128,49 +128,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&fin), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    const RowBlocks blocks{128};
     if (warp == 0) {
         for (int i = 0; i < kRowMaps && a.box << i <= 128; i++) tma_prefetch(&tm_a.m[i]);
+    } else if (warp == 1) {
+        tmem_alloc<1>(smem_u32(&s_tmem), 512);
     } else if (warp == 2) {
         tma_prefetch(&tm_b);
+    } else if (warp >= 4) {
+        build_plan<32 * kEpi>(a.offsets, a.E, a.rows, blocks, tab, s_scan, &s_live);
     }
-    if (warp == 1) tmem_alloc<1>(smem_u32(&s_tmem), 512);
     fence_before();
-    const RowBlocks blocks{128};
-    const int live = build_plan(a.offsets, a.E, a.rows, blocks, tab, s_scan);
+    __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
-    PlanWalk tiles(tab, live, blocks, (a.M + NF - 1) / NF, blockIdx.x, gridDim.x);
+    PlanWalk tiles(tab, s_live, blocks, (a.M + NF - 1) / NF, blockIdx.x, gridDim.x);
     PlanTile v;
 
     if (warp < 4) {
         if (SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
-        if (warp == 0 || warp == 2) {
-            // ============ copies: warp 0 the rows (A), warp 2 the weights (B)
-            const bool is_a = warp == 0;
+        if (warp == 0) {
+            // ============ copies of the rows (A)
             if (elect1()) {
-                int st = 0;
-                uint32_t ph = 0;
-                long long issued = 0;
-                bool ok = true;
-                while (ok && tiles.next(v)) {
-                    const int ua = row_units(v.n, a.box);
-                    const uint32_t bytes = is_a ? (uint32_t)(ua * a.box * 128) : NF * 128;
-                    for (int b = 0; b < a.blocks; b++) {
-                        if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_v, a.wait, err))) break;
-                        const uint32_t bar = smem_u32(&full[st]), sa = smem_u32(ring + (size_t)st * STAGE);
-                        if (!(a.withhold && blockIdx.x == 0 && issued == 0)) {   // testing: never filled, so the wait runs out
-                            mbar_expect_tx(bar, bytes);
-                            if (is_a) tma_rows(sa, tm_a, 128 * b, v.r0, ua, a.box, bar);
-                            else tma_3d(sa + kABytes, &tm_b, 128 * b, v.m * NF, v.e, bar);
-                        }
-                        issued++;
-                        if (++st == a.stages) { st = 0; ph ^= 1; }
-                    }
-                }
-                s_issued[is_a] = issued;
+                int ua = 0;
+                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
+                                 [&] {
+                                     if (!tiles.next(v)) return -1;
+                                     ua = row_units(v.n, a.box);
+                                     return a.blocks;
+                                 },
+                                 [&](int b, uint32_t bar, uint32_t sa) {
+                                     mbar_expect_tx(bar, (uint32_t)(ua * a.box * 128));
+                                     tma_rows(sa, tm_a, 128 * b, v.r0, ua, a.box, bar);
+                                 });
             }
             __syncwarp();
-            drain_copies(full, a.stages, s_issued, is_a, a.withhold && blockIdx.x == 0, err);
+            drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
+        } else if (warp == 2) {
+            // ============ copies of the weights (B)
+            if (elect1())
+                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
+                                 [&] { return tiles.next(v) ? a.blocks : -1; },
+                                 [&](int b, uint32_t bar, uint32_t sa) {
+                                     mbar_expect_tx(bar, NF * 128);
+                                     tma_3d(sa + kABytes, &tm_b, 128 * b, v.m * NF, v.e, bar);
+                                 });
+            __syncwarp();
+            drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 1) {
             // ============ MMAs: one accumulator per block
             if (elect1()) {

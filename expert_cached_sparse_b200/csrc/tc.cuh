@@ -156,21 +156,55 @@ template <int N>   // all but the newest N groups have read their source
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// End of the two copy warps of a CTA (converged, `is_a` one of them): every
-// issued copy lands before the CTA exits.  After an abort one warp may be
-// ahead; the other arrives for the stages it did not fill, so that their
-// phases complete with the copies in flight.  `withheld`: the CTA's first
-// stage never completes (a test's doing).
-__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, volatile long long* issued, bool is_a,
-                                             bool withheld, int* error)
+// Where a copy warp stands: copies issued, next stage, its phase bit.
+struct CopyPos {
+    long long issued;
+    int st;
+    uint32_t ph;
+};
+// A copy warp's loop over the stages of its tiles, walked by one thread:
+// next() gives the steps of the next tile or -1, issue(s, bar, stage) starts
+// the copies of step s and announces their bytes on the stage's barrier.
+// `withheld`: the first stage is never filled (a test's doing).
+template <int STAGE, class NEXT, class ISSUE>
+__device__ __forceinline__ void copy_loop(uint64_t* full, uint64_t* empty, unsigned char* ring, int stages,
+                                          volatile int* abort_flag, long long limit, bool withheld, int* error,
+                                          volatile CopyPos* end, NEXT next, ISSUE issue)
+{
+    int st = 0, steps;
+    uint32_t ph = 0;
+    long long issued = 0;
+    bool ok = true;
+    while (ok && (steps = next()) >= 0)
+        for (int s = 0; s < steps; s++) {
+            if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_flag, limit, error))) break;
+            if (withheld) withheld = false;
+            else issue(s, smem_u32(&full[st]), smem_u32(ring) + (uint32_t)(st * STAGE));
+            issued++;
+            if (++st == stages) { st = 0; ph ^= 1; }
+        }
+    end->issued = issued;
+    end->st = st;
+    end->ph = ph;
+}
+// End of the two copy warps of a CTA (converged): every issued copy lands
+// before the CTA exits.  After an abort one warp may be ahead; the other
+// arrives for the stages it did not fill, so that their phases complete with
+// the copies in flight.  No divisions: this is on every call's way out.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, volatile CopyPos* end, int mine, bool withheld,
+                                             int* error)
 {
     asm volatile("bar.sync 1, 64;" ::: "memory");
-    const long long mine = issued[is_a], most = max(mine, issued[!is_a]);
-    if ((threadIdx.x & 31) == 0)
-        for (long long i = mine; i < most; i++) mbar_arrive(smem_u32(&full[i % stages]));
-    if (is_a)
-        for (long long i = most > stages ? most - stages : 0; i < most; i++)
-            if (i > 0 || !withheld) mbar_drain(smem_u32(&full[i % stages]), (uint32_t)(i / stages) & 1, error);
+    int st = end[mine].st, behind = (int)max(0ll, end[!mine].issued - end[mine].issued);
+    uint32_t ph = end[mine].ph;
+    const long long most = end[mine].issued + behind;
+    for (; behind > 0; behind--) {
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&full[st]));
+        if (++st == stages) { st = 0; ph ^= 1; }
+    }
+    if (mine == 0)   // stage i was last filled in this pass over the ring if i < st, else in the previous one
+        for (int i = 0; i < stages && i < most; i++)
+            if (!(withheld && i == 0)) mbar_drain(smem_u32(&full[i]), i < st ? ph : (ph ^ 1), error);
 }
 
 // ------------------------------------------------------------------ tcgen05
@@ -359,13 +393,15 @@ __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets,
 __host__ __device__ static inline int plan_bytes(int E) { return (int)align_up(sizeof(PlanExpert) * (E + 1), 128); }
 
 // Builds the table in shared memory: the experts with rows in ascending order,
-// then a closing entry {blocks in all}.  Called by all threads; returns the
-// number of experts.  Ranges that overlap so often that the blocks pass 2^31
-// void the call.
-__device__ __forceinline__ int build_plan(const int32_t* __restrict__ offsets, int E, int rows, const RowBlocks& B,
-                                          PlanExpert* tab, long long* scratch)
+// then a closing entry {blocks in all}, and their number in *live.  Called by
+// the last NT threads of the CTA, beside what the first ones set up; a barrier
+// of the CTA has to follow.  Ranges that overlap so often that the blocks pass
+// 2^31 void the call.
+template <int NT>
+__device__ __forceinline__ void build_plan(const int32_t* __restrict__ offsets, int E, int rows, const RowBlocks& B,
+                                           PlanExpert* tab, long long* scratch, int* live)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int tid = threadIdx.x - (blockDim.x - NT), lane = tid & 31, warp = tid >> 5, nt = NT;
     const int per = (E + nt - 1) / nt, e0 = min(E, tid * per), e1 = min(E, e0 + per);
     // experts in the low 13 bits, blocks above: one sum for both
     long long sum = 0;
@@ -380,14 +416,15 @@ __device__ __forceinline__ int build_plan(const int32_t* __restrict__ offsets, i
         if (lane >= o) in += x;
     }
     if (lane == 31) scratch[warp] = in;
-    __syncthreads();
+    asm volatile("bar.sync 2, %0;" ::"n"(NT) : "memory");
     long long base = in - sum, total = 0;
-    for (int w = 0; w < nt / 32; w++) {
+#pragma unroll
+    for (int w = 0; w < NT / 32; w++) {
         if (w < warp) base += scratch[w];
         total += scratch[w];
     }
     const bool voided = total >> 13 > 0x7fffffff;
-    const int live = voided ? 0 : (int)(total & 8191);
+    const int n = voided ? 0 : (int)(total & 8191);
     if (!voided)
         for (int e = e0; e < e1; e++) {
             int lo, hi;
@@ -396,9 +433,10 @@ __device__ __forceinline__ int build_plan(const int32_t* __restrict__ offsets, i
             tab[base & 8191] = {(int)(base >> 13), e, lo, hi};
             base += ((long long)B.blocks(hi - lo) << 13) + 1;
         }
-    if (tid == 0) tab[live] = {voided ? 0 : (int)(total >> 13), 0, 0, 0};
-    __syncthreads();
-    return live;
+    if (tid == 0) {
+        tab[n] = {voided ? 0 : (int)(total >> 13), 0, 0, 0};
+        *live = n;
+    }
 }
 
 // A tile: the m-th feature tile of expert e, n rows from r0 on.

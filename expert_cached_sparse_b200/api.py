@@ -240,10 +240,11 @@ def moe_prefill_forward(cache: MoeCache, layer0, xs, wgs, biases, outs, ws, stre
 
 
 # ------------------------------------------------------------------ expert matrix products
-# These calls are short next to a Python check per argument, so the checks of a
-# call are a few comparisons; _refuse works out which one failed.
+# These calls are short next to a Python call per check, so a call unpacks the
+# shapes and strides and compares; _refuse works out which argument failed.
 _BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 _OUT = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+_NOT_AS_REQUIRED = (AttributeError, TypeError, ValueError)   # of unpacking what is no tensor, or of other dimensions
 
 
 def _refuse(fn, **specs):
@@ -259,29 +260,25 @@ def _refuse(fn, **specs):
             raise ValueError(f"{fn}: {name} must have shape {want}, got {list(t.shape)}")
         if packed and not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
-        if not packed and _ld(t) < 0:
+        if not packed and not _ld(t.stride(), *t.shape):
             raise ValueError(f"{fn}: {name} must have adjacent columns and rows that do not overlap, got strides {t.stride()}")
     for name, (t, *_) in specs.items():
         if t.get_device() != _device():
             raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
-    raise AssertionError(fn)
+    raise ValueError(f"{fn}: arguments do not fit together")
 
 
-def _ld(t) -> int:
-    """Leading dimension of a row matrix whose columns are adjacent, -1 of any other."""
-    rows, cols = t.shape
-    a, b = t.stride()
-    if b != 1 and cols > 1:
-        return -1
-    return cols if rows <= 1 else a if a >= cols else -1
+def _dims(t, n):
+    """t's shape if it is a tensor of n dimensions, else n Nones."""
+    return tuple(t.shape) if isinstance(t, torch.Tensor) and t.dim() == n else (None,) * n
 
 
-def _dims(*pairs) -> bool:
-    """Whether every (argument, dimensions) is a tensor of that many dimensions."""
-    for t, d in pairs:
-        if not isinstance(t, torch.Tensor) or t.dim() != d:
-            return False
-    return True
+def _ld(strides, rows, cols) -> int:
+    """Leading dimension of a row matrix whose columns are adjacent, 0 of any other."""
+    a, b = strides
+    if b != 1:
+        return 0
+    return a if a >= cols else cols if rows <= 1 else 0
 
 
 def _device() -> int:
@@ -294,13 +291,17 @@ def moe_grouped_gemm(x, w, offsets, y, stream=None):
 
     x [rows, in] bf16, w [experts, out, in] bf16, offsets int32 [experts + 1], y [rows, out]
     float32 or bf16; x and y may be column slices of wider matrices."""
-    E, N, K = w.shape if _dims((w, 3)) else (None, None, None)
-    rows = x.shape[0] if _dims((x, 2)) else None
-    if not (_dims((offsets, 1), (y, 2)) and E is not None and rows is not None
-            and x.dtype is _BF16 and w.dtype is _BF16 and offsets.dtype is _I32 and y.dtype in _OUT
-            and x.shape[1] == K and offsets.shape[0] == E + 1 and y.shape == (rows, N)
-            and w.is_contiguous() and offsets.is_contiguous() and (ldx := _ld(x)) >= 0 and (ldy := _ld(y)) >= 0
-            and x.get_device() == w.get_device() == offsets.get_device() == y.get_device() == _device()):
+    try:
+        (E, N, K), (rows, kx), (ne,), (ry, ny) = w.shape, x.shape, offsets.shape, y.shape
+        ldx, ldy = _ld(x.stride(), rows, K), _ld(y.stride(), rows, N)
+        good = (ldx and ldy and kx == K and ne == E + 1 and ry == rows and ny == N
+                and x.dtype is _BF16 and w.dtype is _BF16 and offsets.dtype is _I32 and y.dtype in _OUT
+                and w.is_contiguous() and offsets.is_contiguous()
+                and x.get_device() == w.get_device() == offsets.get_device() == y.get_device() == _device())
+    except _NOT_AS_REQUIRED:
+        good = False
+    if not good:
+        (E, N, K), (rows, _) = _dims(w, 3), _dims(x, 2)
         _refuse("moe_grouped_gemm", w=(w, (_BF16,), (None, None, None), True), x=(x, (_BF16,), (None, K), False),
                 offsets=(offsets, (_I32,), (E and E + 1,), True), y=(y, _OUT, (rows, N), False))
     rc = L.lib.moe_grouped_gemm(E, K, N, x.data_ptr(), ldx, w.data_ptr(), offsets.data_ptr(), rows, y.data_ptr(), ldy,
@@ -312,13 +313,17 @@ def moe_grouped_gemm_dx(dy, w, offsets, dx, stream=None):
     """Gradient of moe_grouped_gemm with respect to x: dx[r] = W_e^T dy[r].
 
     dy [rows, out] bf16, w [experts, out, in] bf16, dx [rows, in] float32 or bf16."""
-    E, N, K = w.shape if _dims((w, 3)) else (None, None, None)
-    rows = dy.shape[0] if _dims((dy, 2)) else None
-    if not (_dims((offsets, 1), (dx, 2)) and E is not None and rows is not None
-            and dy.dtype is _BF16 and w.dtype is _BF16 and offsets.dtype is _I32 and dx.dtype in _OUT
-            and dy.shape[1] == N and offsets.shape[0] == E + 1 and dx.shape == (rows, K)
-            and w.is_contiguous() and offsets.is_contiguous() and (lddy := _ld(dy)) >= 0 and (lddx := _ld(dx)) >= 0
-            and dy.get_device() == w.get_device() == offsets.get_device() == dx.get_device() == _device()):
+    try:
+        (E, N, K), (rows, ny), (ne,), (rx, kx) = w.shape, dy.shape, offsets.shape, dx.shape
+        lddy, lddx = _ld(dy.stride(), rows, N), _ld(dx.stride(), rows, K)
+        good = (lddy and lddx and ny == N and ne == E + 1 and rx == rows and kx == K
+                and dy.dtype is _BF16 and w.dtype is _BF16 and offsets.dtype is _I32 and dx.dtype in _OUT
+                and w.is_contiguous() and offsets.is_contiguous()
+                and dy.get_device() == w.get_device() == offsets.get_device() == dx.get_device() == _device())
+    except _NOT_AS_REQUIRED:
+        good = False
+    if not good:
+        (E, N, K), (rows, _) = _dims(w, 3), _dims(dy, 2)
         _refuse("moe_grouped_gemm_dx", w=(w, (_BF16,), (None, None, None), True), dy=(dy, (_BF16,), (None, N), False),
                 offsets=(offsets, (_I32,), (E and E + 1,), True), dx=(dx, _OUT, (rows, K), False))
     rc = L.lib.moe_grouped_gemm_dx(E, K, N, dy.data_ptr(), lddy, w.data_ptr(), offsets.data_ptr(), rows, dx.data_ptr(),
@@ -331,13 +336,17 @@ def moe_grouped_gemm_dw(dy, x, offsets, dw, accumulate=False, stream=None):
 
     dy [rows, out] bf16, x [rows, in] bf16, dw [experts, out, in] float32 or bf16; accumulate
     adds to what dw holds instead of storing."""
-    E, N, K = dw.shape if _dims((dw, 3)) else (None, None, None)
-    rows = dy.shape[0] if _dims((dy, 2)) else None
-    if not (_dims((offsets, 1), (x, 2)) and E is not None and rows is not None
-            and dy.dtype is _BF16 and x.dtype is _BF16 and offsets.dtype is _I32 and dw.dtype in _OUT
-            and dy.shape[1] == N and x.shape == (rows, K) and offsets.shape[0] == E + 1
-            and dw.is_contiguous() and offsets.is_contiguous() and (lddy := _ld(dy)) >= 0 and (ldx := _ld(x)) >= 0
-            and dy.get_device() == x.get_device() == offsets.get_device() == dw.get_device() == _device()):
+    try:
+        (E, N, K), (rows, ny), (rx, kx), (ne,) = dw.shape, dy.shape, x.shape, offsets.shape
+        lddy, ldx = _ld(dy.stride(), rows, N), _ld(x.stride(), rows, K)
+        good = (lddy and ldx and ny == N and rx == rows and kx == K and ne == E + 1
+                and dy.dtype is _BF16 and x.dtype is _BF16 and offsets.dtype is _I32 and dw.dtype in _OUT
+                and dw.is_contiguous() and offsets.is_contiguous()
+                and dy.get_device() == x.get_device() == offsets.get_device() == dw.get_device() == _device())
+    except _NOT_AS_REQUIRED:
+        good = False
+    if not good:
+        (E, N, K), (rows, _) = _dims(dw, 3), _dims(dy, 2)
         _refuse("moe_grouped_gemm_dw", dw=(dw, _OUT, (None, None, None), True), dy=(dy, (_BF16,), (None, N), False),
                 x=(x, (_BF16,), (rows, K), False), offsets=(offsets, (_I32,), (E and E + 1,), True))
     rc = L.lib.moe_grouped_gemm_dw(E, K, N, dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows,
@@ -348,17 +357,22 @@ def moe_grouped_gemm_dw(dy, x, offsets, dw, accumulate=False, stream=None):
 def moe_grouped_gemm_fp8(xq, xs, wq, ws, offsets, y, stream=None):
     """moe_grouped_gemm of e4m3 codes: xq [rows, in] with scales xs [ceil(in/128), rows], wq
     [experts, out, in] with scales ws [experts, ceil(out/128), ceil(in/128)] (float32)."""
-    E, N, K = wq.shape if _dims((wq, 3)) else (None, None, None)
-    rows = xq.shape[0] if _dims((xq, 2)) else None
-    nb, kb = (None, None) if E is None else ((N + 127) // 128, (K + 127) // 128)
-    if not (_dims((xs, 2), (ws, 3), (offsets, 1), (y, 2)) and E is not None and rows is not None
-            and xq.dtype is _E4M3 and wq.dtype is _E4M3 and xs.dtype is _F32 and ws.dtype is _F32
-            and offsets.dtype is _I32 and y.dtype in _OUT and xq.shape[1] == K and xs.shape == (kb, rows)
-            and ws.shape == (E, nb, kb) and offsets.shape[0] == E + 1 and y.shape == (rows, N)
-            and xs.is_contiguous() and wq.is_contiguous() and ws.is_contiguous() and offsets.is_contiguous()
-            and (ldxq := _ld(xq)) >= 0 and (ldy := _ld(y)) >= 0
-            and xq.get_device() == xs.get_device() == wq.get_device() == ws.get_device() == offsets.get_device()
-            == y.get_device() == _device()):
+    try:
+        (E, N, K), (rows, kx), (ne,), (ry, ny) = wq.shape, xq.shape, offsets.shape, y.shape
+        nb, kb = (N + 127) // 128, (K + 127) // 128
+        ldxq, ldy = _ld(xq.stride(), rows, K), _ld(y.stride(), rows, N)
+        good = (ldxq and ldy and kx == K and ne == E + 1 and ry == rows and ny == N
+                and xs.shape == (kb, rows) and ws.shape == (E, nb, kb)
+                and xq.dtype is _E4M3 and wq.dtype is _E4M3 and xs.dtype is _F32 and ws.dtype is _F32
+                and offsets.dtype is _I32 and y.dtype in _OUT
+                and xs.is_contiguous() and wq.is_contiguous() and ws.is_contiguous() and offsets.is_contiguous()
+                and xq.get_device() == xs.get_device() == wq.get_device() == ws.get_device() == offsets.get_device()
+                == y.get_device() == _device())
+    except _NOT_AS_REQUIRED:
+        good = False
+    if not good:
+        (E, N, K), (rows, _) = _dims(wq, 3), _dims(xq, 2)
+        nb, kb = (None, None) if E is None else ((N + 127) // 128, (K + 127) // 128)
         _refuse("moe_grouped_gemm_fp8", wq=(wq, (_E4M3,), (None, None, None), True), xq=(xq, (_E4M3,), (None, K), False),
                 xs=(xs, (_F32,), (kb, rows), True), ws=(ws, (_F32,), (E, nb, kb), True),
                 offsets=(offsets, (_I32,), (E and E + 1,), True), y=(y, _OUT, (rows, N), False))
@@ -370,12 +384,18 @@ def moe_grouped_gemm_fp8(xq, xs, wq, ws, offsets, y, stream=None):
 def moe_fp8_quantize_act(x, q, s, swiglu=False, stream=None):
     """e4m3 codes q [rows, cols] and scales s [ceil(cols/128), rows] of x [rows, cols] (float32 or
     bf16), or with swiglu of silu(gate) * up of x [rows, 2 cols] = gate | up."""
-    rows, cols = q.shape if _dims((q, 2)) else (None, None)
-    width, kb = (None, None) if cols is None else (2 * cols if swiglu else cols, (cols + 127) // 128)
-    if not (_dims((x, 2), (s, 2)) and cols is not None and q.dtype is _E4M3 and x.dtype in _OUT and s.dtype is _F32
-            and x.shape == (rows, width) and s.shape == (kb, rows) and s.is_contiguous()
-            and (ldx := _ld(x)) >= 0 and (ldq := _ld(q)) >= 0
-            and x.get_device() == q.get_device() == s.get_device() == _device()):
+    try:
+        (rows, cols), (rx, width) = q.shape, x.shape
+        ldx, ldq = _ld(x.stride(), rows, width), _ld(q.stride(), rows, cols)
+        good = (ldx and ldq and rx == rows and width == (2 * cols if swiglu else cols)
+                and s.shape == ((cols + 127) // 128, rows)
+                and q.dtype is _E4M3 and x.dtype in _OUT and s.dtype is _F32 and s.is_contiguous()
+                and x.get_device() == q.get_device() == s.get_device() == _device())
+    except _NOT_AS_REQUIRED:
+        good = False
+    if not good:
+        rows, cols = _dims(q, 2)
+        width, kb = (None, None) if cols is None else (2 * cols if swiglu else cols, (cols + 127) // 128)
         _refuse("moe_fp8_quantize_act", q=(q, (_E4M3,), (None, None), False), x=(x, _OUT, (rows, width), False),
                 s=(s, (_F32,), (kb, rows), True))
     rc = L.lib.moe_fp8_quantize_act(x.data_ptr(), _OUT[x.dtype], ldx, rows, cols, 1 if swiglu else 0, q.data_ptr(), ldq,
@@ -386,12 +406,17 @@ def moe_fp8_quantize_act(x, q, s, swiglu=False, stream=None):
 def moe_fp8_quantize_weight(w, q, s, stream=None):
     """e4m3 codes q and 128 x 128 block scales s [experts, ceil(out/128), ceil(in/128)] of w
     [experts, out, in] (float32 or bf16)."""
-    E, N, K = w.shape if _dims((w, 3)) else (None, None, None)
-    nb, kb = (None, None) if E is None else ((N + 127) // 128, (K + 127) // 128)
-    if not (_dims((q, 3), (s, 3)) and E is not None and w.dtype in _OUT and q.dtype is _E4M3 and s.dtype is _F32
-            and q.shape == (E, N, K) and s.shape == (E, nb, kb)
-            and w.is_contiguous() and q.is_contiguous() and s.is_contiguous()
-            and w.get_device() == q.get_device() == s.get_device() == _device()):
+    try:
+        E, N, K = w.shape
+        good = (q.shape == (E, N, K) and s.shape == (E, (N + 127) // 128, (K + 127) // 128)
+                and w.dtype in _OUT and q.dtype is _E4M3 and s.dtype is _F32
+                and w.is_contiguous() and q.is_contiguous() and s.is_contiguous()
+                and w.get_device() == q.get_device() == s.get_device() == _device())
+    except _NOT_AS_REQUIRED:
+        good = False
+    if not good:
+        E, N, K = _dims(w, 3)
+        nb, kb = (None, None) if E is None else ((N + 127) // 128, (K + 127) // 128)
         _refuse("moe_fp8_quantize_weight", w=(w, _OUT, (None, None, None), True), q=(q, (_E4M3,), (E, N, K), True),
                 s=(s, (_F32,), (E, nb, kb), True))
     rc = L.lib.moe_fp8_quantize_weight(w.data_ptr(), _OUT[w.dtype], E, N, K, q.data_ptr(), s.data_ptr(),

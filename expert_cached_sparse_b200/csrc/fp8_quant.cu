@@ -63,8 +63,18 @@ __device__ __forceinline__ float max8(const float (&v)[8])
     return m;
 }
 
-// silu(g) * u: expf within 2 units in the last place, the quotient too.
-__device__ __forceinline__ float swiglu1(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+// silu(g) * u with the hardware's 2^x (relative error 2^-22) and reciprocal
+// (2^-23): with the roundings of -g log2(e), of the sum and of the products
+// the relative error is below (10 + 1.5 |g|) 2^-24, far inside an e4m3 step of
+// 2^-4.  Six instructions an element; expf and a division took 32 in all, and
+// this kernel is bound by its instructions (44% of HBM, 79% of issue slots).
+__device__ __forceinline__ float swiglu1(float g, float u)
+{
+    float t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return g * r * u;
+}
 
 // The block's divisor: v / s for its 128 or 16384 elements by Markstein's
 // method (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with y the correctly

@@ -498,14 +498,14 @@ template <int MODE, int NB, int CG>
 int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NB / CG * 128;
+    static std::atomic<int> smem_set[kMaxDevices];
+    auto* kern = gg_kernel<MODE, NB, CG>;
     int sms = 0;
-    if (int rc = device_sms(&sms)) return rc;
+    if (int rc = prepare_launch(kern, smem_set, &sms)) return rc;
     const int fixed = MODE == DW ? kStaging + (int)align_up(4 * (a.E + 1), 128) : plan_bytes(a.E);
     a.stages = (kSmemMax - 1024 - fixed) / STAGE;                    // 1 KB static
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = fixed + a.stages * STAGE;
-    auto* kern = gg_kernel<MODE, NB, CG>;
-    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
     MOE_CUDA_TRY(launch_clusters(kern, sms, CG, kThreads, smem, st, ta, tb, to, a));

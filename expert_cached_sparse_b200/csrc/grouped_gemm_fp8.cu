@@ -299,13 +299,14 @@ template <int NF>
 int launch(Args& a, const RowMaps& ta, const CUtensorMap& tb, cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NF * 128;
+    static std::atomic<int> smem_set[kMaxDevices];
+    auto* kern = gg8_kernel<NF>;
     int sms = 0;
-    if (int rc = device_sms(&sms)) return rc;
+    if (int rc = prepare_launch(kern, smem_set, &sms)) return rc;
     const int fixed = plan_bytes(a.E);
     a.stages = (kSmemMax - 1024 - fixed) / STAGE;   // 1 KB static
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = fixed + a.stages * STAGE;
-    auto* kern = gg8_kernel<NF>;
     if (NF == 256) {   // the register split counts on what the kernel was compiled to
         static const int regs = [] {
             cudaFuncAttributes at{};
@@ -313,7 +314,6 @@ int launch(Args& a, const RowMaps& ta, const CUtensorMap& tb, cudaStream_t st)
         }();
         if (regs != kRegs) return MOE_ERR_UNSUPPORTED;
     }
-    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
     MOE_CUDA_TRY(launch_clusters(kern, sms, 1, kThreads, smem, st, ta, tb, a));

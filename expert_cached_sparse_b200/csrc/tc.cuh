@@ -5,6 +5,8 @@
 // instruction four MMAs take 61 cycles to issue instead of 163.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 
 #include "common.cuh"
@@ -527,11 +529,23 @@ static inline bool rows_ok(const void* p, int64_t ld, int64_t width, int size)
 static inline bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_BF16; }
 static inline int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
 
-static inline int device_sms(int* sms)
+// SMs of the current device.  The first launch of a kernel on a device also
+// lets it use all of an SM's shared memory (`smem_set`: one flag a device).
+template <class K>
+static inline int prepare_launch(K* kern, std::atomic<int>* smem_set, int* sms)
 {
+    static std::atomic<int> count[kMaxDevices];
     int dev = 0;
     MOE_CUDA_TRY(cudaGetDevice(&dev));
-    MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+    if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+    if (!(*sms = count[dev].load(std::memory_order_relaxed))) {
+        MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+        count[dev].store(*sms, std::memory_order_relaxed);
+    }
+    if (!smem_set[dev].load(std::memory_order_relaxed)) {
+        MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 1024));
+        smem_set[dev].store(1, std::memory_order_relaxed);
+    }
     return MOE_OK;
 }
 

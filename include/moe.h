@@ -583,7 +583,8 @@ int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, const uint8_t
  * Rows -> e4m3 codes with one float32 scale per 128 columns of a row (the
  * last block may be shorter).  With swiglu == 0 the row is d_x [rows][cols]
  * (x_dtype, ldx); otherwise d_x is [rows][2 cols], gate then up, and the row
- * is silu(gate) * up in fp32, not rounded in between.  For a block of
+ * is silu(gate) * up in fp32 (relative error below (10 + 1.5 |gate|) 2^-24),
+ * not rounded in between.  For a block of
  * largest magnitude m (NaN left out): s = m / 448, or 1 when m < 2^-100;
  * q = the e4m3 code nearest to x / s (ties to even), division and quotient in
  * fp32; codes of a block below 2^-100 are zeros.  A NaN becomes a NaN code;

@@ -45,6 +45,7 @@ using namespace tc;
 
 constexpr int kThreads = 256;
 constexpr int kMaxStages = 12;
+constexpr int kStatic = 1024;        // bytes of static shared memory at most
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
 constexpr int kStaging = 4 * 2 * 4096;
 
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect1())
             copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
                              [&] { return units.next(v) ? v.steps : -1; },
-                             [&](int s, uint32_t bar, uint32_t sa) {
+                             [&](int s, uint32_t bar, uint32_t sa, int) {
                                  const int k = v.k0 + 64 * s;
                                  mbar_expect_tx(bar, kABytes);
                                  if (MODE == FWD) {
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  bytes = (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
                                  return v.steps;
                              },
-                             [&](int s, uint32_t bar, uint32_t sa) {
+                             [&](int s, uint32_t bar, uint32_t sa, int) {
                                  const int k = v.k0 + 64 * s;
                                  const uint32_t sb = sa + kABytes;
                                  if (PAIR && bytes == 0) {   // a pair's second half without columns
@@ -501,9 +502,9 @@ int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorM
     static std::atomic<int> smem_set[kMaxDevices];
     auto* kern = gg_kernel<MODE, NB, CG>;
     int sms = 0;
-    if (int rc = prepare_launch(kern, smem_set, &sms)) return rc;
+    if (int rc = prepare_launch(kern, kSmemMax - kStatic, smem_set, &sms)) return rc;
     const int fixed = MODE == DW ? kStaging + (int)align_up(4 * (a.E + 1), 128) : plan_bytes(a.E);
-    a.stages = (kSmemMax - 1024 - fixed) / STAGE;                    // 1 KB static
+    a.stages = (kSmemMax - kStatic - fixed) / STAGE;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = fixed + a.stages * STAGE;
     ProfScope ps(MOE_PROF_GEMM, st);

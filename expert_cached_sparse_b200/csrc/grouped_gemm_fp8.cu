@@ -6,22 +6,24 @@
 // The scales are arbitrary, so they cannot go into the tensor core (its block
 // scales are powers of two): each 128-column block is a product of its own in
 // tensor memory, and the epilogue adds it, scaled, to fp32 sums in registers.
-// Rows are the tensor core's M, one tensor-memory lane and one thread each,
-// and features its N: a thread's scale xs ws is then one number for all of its
-// columns, and an element costs one FMA.  (With features as M and rows as N,
-// as in grouped_gemm.cu, every column has its own scale, and reading those
-// from shared memory takes as long as the FMAs: 575 against 329 cycles for
-// 128 x 256 elements, 16 warps.)  An expert of few rows computes 128 all the
-// same, but 128 x 128 x 128 take 256 cycles and the weights' 16 KB come from
-// HBM at the rate of one such tile in 700, and only warps with rows add.
+//
+// MANY rows an expert: rows are the tensor core's M, one tensor-memory lane
+// and one thread each, and 256 features its N: a thread's scale xs ws is then
+// one number for all of its columns, and an element costs one FMA.  (With rows
+// as N every column has its own scale, and reading those from shared memory
+// takes as long as the FMAs: 575 against 329 cycles for 128 x 256 elements, 16
+// warps.)
+// FEW: features are M and up to 32 rows N, as in grouped_gemm.cu, so that all
+// warps have work on a tile of one row and the MMAs compute 16 rows and not
+// 128: 120 W less at the same stream of weights, which the clock gets back.
 //
 // Roles, one persistent CTA per SM: warps 0 and 2 copy (one 128-column block
 // of rows and of weights per stage, TMA into the 128-byte swizzle), warp 1
-// issues the MMAs of a block into one of the accumulators, and warps 4-11 add,
-// a quarter of the rows and half of the columns each.  (On pairs of CTAs, as
-// in grouped_gemm.cu, every block's accumulator has to be handed back across
-// the cluster: 1.26 ms against 0.89 for 4096 tokens.)  Waits are bounded as in
-// grouped_gemm.cu.
+// issues the MMAs of a block into one of the accumulators, and warps 4 on add,
+// a quarter of the lanes each (MANY: and half of the columns).  (On pairs of
+// CTAs, as in grouped_gemm.cu, every block's accumulator has to be handed back
+// across the cluster: 1.26 ms against 0.89 for 4096 tokens.)  Waits are
+// bounded as in grouped_gemm.cu.
 #include "tc.cuh"
 
 namespace moe {
@@ -32,16 +34,25 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
-constexpr int kEpi = 8;              // epilogue warps
+template <bool FEW_>
+struct Cfg {
+    static constexpr bool FEW = FEW_;
+    static constexpr int NF = FEW ? 128 : 256;              // features of a tile
+    static constexpr int NR = FEW ? 32 : 128;               // most rows of a tile
+    static constexpr int EPI = FEW ? 4 : 8;                 // epilogue warps
+    static constexpr int THREADS = 128 + 32 * EPI;
+    static constexpr int COLS = FEW ? NR : NF;              // tensor-memory columns of an accumulator
+    static constexpr int BUFS = FEW ? 4 : 512 / COLS;       // accumulators
+    static constexpr int CW = FEW ? COLS : COLS / 2;        // columns of one epilogue warp
+    static constexpr int WEIGHTS = NF * 128, STAGE = WEIGHTS + NR * 128;
+};
 // Registers a thread of the control warps and of the epilogue's where the
 // latter hold 128 sums each: together what the block is launched with,
 // 128 * 72 + 256 * 216 = 384 * 168.
 constexpr int kRegs = 168, kControlRegs = 72, kSumRegs = 216;
-static_assert(128 * kControlRegs + 32 * kEpi * kSumRegs <= kThreads * kRegs, "a larger split never starts");
-
+static_assert(128 * kControlRegs + 32 * Cfg<false>::EPI * kSumRegs <= Cfg<false>::THREADS * kRegs, "a larger split never starts");
 constexpr int kMaxStages = 12;
-constexpr int kABytes = 128 * 128;   // 128 rows x 128 columns
+constexpr int kStatic = 4096;        // bytes of static shared memory at most
 
 struct Args {
     const int32_t* offsets;
@@ -89,22 +100,21 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
     }
 }
 
-// Tiles of 128 rows by NF features.
-template <int NF>
-__global__ void __launch_bounds__(kThreads, 1)
-    gg8_kernel(const __grid_constant__ RowMaps tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a)
+template <class CFG>
+__global__ void __launch_bounds__(CFG::THREADS, 1)
+    gg8_kernel(const __grid_constant__ RowMaps tm_rows, const __grid_constant__ CUtensorMap tm_w, const Args a)
 {
-    constexpr int STAGE = kABytes + NF * 128;
-    constexpr int BUFS = 512 / NF;                // accumulators
-    constexpr int CW = NF / 2;                    // columns of one epilogue warp
-    constexpr bool SPLIT = CW > 64;               // registers moved from the control warps to the epilogue's
+    constexpr bool FEW = CFG::FEW;
+    constexpr int NF = CFG::NF, CW = CFG::CW, BUFS = CFG::BUFS, STAGE = CFG::STAGE, WEIGHTS = CFG::WEIGHTS;
+    constexpr uint32_t TMEM = BUFS * CFG::COLS;
     constexpr int GROUP = 4;                      // blocks whose scales are fetched together, a group ahead
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[BUFS], acc_empty[BUFS], fin;
     __shared__ uint32_t s_tmem;
     __shared__ CopyPos s_copy[2];
     __shared__ int s_abort, s_live;
-    __shared__ long long s_scan[kEpi];
+    __shared__ long long s_scan[CFG::EPI];
+    __shared__ __align__(16) float s_scale[FEW ? CFG::EPI : 1][GROUP][32];   // FEW: a warp's scales of a group
     unsigned char* ring = smem_raw;
     PlanExpert* tab = reinterpret_cast<PlanExpert*>(ring + (size_t)a.stages * STAGE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -123,20 +133,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < BUFS; i++) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), kEpi);
+            mbar_init(smem_u32(&acc_empty[i]), CFG::EPI);
         }
         mbar_init(smem_u32(&fin), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const RowBlocks blocks{128};
+    const RowBlocks blocks{CFG::NR};
     if (warp == 0) {
-        for (int i = 0; i < kRowMaps && a.box << i <= 128; i++) tma_prefetch(&tm_a.m[i]);
+        for (int i = 0; i < kRowMaps && a.box << i <= CFG::NR; i++) tma_prefetch(&tm_rows.m[i]);
     } else if (warp == 1) {
-        tmem_alloc<1>(smem_u32(&s_tmem), 512);
+        tmem_alloc<1>(smem_u32(&s_tmem), TMEM);
     } else if (warp == 2) {
-        tma_prefetch(&tm_b);
+        tma_prefetch(&tm_w);
     } else if (warp >= 4) {
-        build_plan<32 * kEpi>(a.offsets, a.E, a.rows, blocks, tab, s_scan, &s_live);
+        build_plan<32 * CFG::EPI>(a.offsets, a.E, a.rows, blocks, tab, s_scan, &s_live);
     }
     fence_before();
     __syncthreads();
@@ -146,32 +156,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     PlanTile v;
 
     if (warp < 4) {
-        if (SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (warp == 0) {
-            // ============ copies of the rows (A)
+            // ============ copies of the rows
             if (elect1()) {
-                int ua = 0;
+                // MANY: a tile's MMAs read 128 rows whatever it has.  Rows left over from a
+                // taller tile, or from before the kernel, are overwritten with zeros (a copy
+                // from behind the matrix) when the stage is next filled: the results do not
+                // depend on them, but the tensor core's power does, and with it the clock.
+                int u = 0;
+                uint64_t tall = ~0ull;   // per stage, 4 bits: boxes that may hold something, less one
                 copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
                                  [&] {
                                      if (!tiles.next(v)) return -1;
-                                     ua = row_units(v.n, a.box);
+                                     u = row_units(v.n, a.box);
                                      return a.blocks;
                                  },
-                                 [&](int b, uint32_t bar, uint32_t sa) {
-                                     mbar_expect_tx(bar, (uint32_t)(ua * a.box * 128));
-                                     tma_rows(sa, tm_a, 128 * b, v.r0, ua, a.box, bar);
+                                 [&](int b, uint32_t bar, uint32_t sa, int st) {
+                                     int wipe = 0;
+                                     if (!FEW) {
+                                         wipe = max(0, min((int)(tall >> (4 * st) & 15) + 1, CFG::NR / a.box) - u);
+                                         tall = (tall & ~(15ull << (4 * st))) | ((uint64_t)(u - 1) << (4 * st));
+                                     }
+                                     const uint32_t sr = sa + WEIGHTS;
+                                     mbar_expect_tx(bar, (uint32_t)((u + wipe) * a.box * 128));
+                                     tma_rows(sr, tm_rows, 128 * b, v.r0, u, a.box, bar);
+                                     if (wipe) tma_rows(sr + u * a.box * 128, tm_rows, 0, a.rows, wipe, a.box, bar);
                                  });
             }
             __syncwarp();
             drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 2) {
-            // ============ copies of the weights (B)
+            // ============ copies of the weights
             if (elect1())
                 copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
                                  [&] { return tiles.next(v) ? a.blocks : -1; },
-                                 [&](int b, uint32_t bar, uint32_t sa) {
-                                     mbar_expect_tx(bar, NF * 128);
-                                     tma_3d(sa + kABytes, &tm_b, 128 * b, v.m * NF, v.e, bar);
+                                 [&](int b, uint32_t bar, uint32_t sa, int) {
+                                     mbar_expect_tx(bar, WEIGHTS);
+                                     tma_3d(sa, &tm_w, 128 * b, v.m * NF, v.e, bar);
                                  });
             __syncwarp();
             drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
@@ -181,17 +203,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int st = 0, buf = 0;
                 uint32_t ph = 0, bph = 0;
                 bool ok = true;
-                const uint32_t id = idesc_e4m3<1>(NF);
                 while (ok && tiles.next(v)) {
+                    const uint32_t id = idesc_e4m3<1>(FEW ? mma_rows<1>(v.n) : NF);
                     for (int b = 0; b < a.blocks; b++) {
                         if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
                         if (!(ok = mbar_wait(smem_u32(&acc_empty[buf]), bph ^ 1, abort_v, a.wait, err))) break;
                         fence_after();
                         const uint32_t sa = smem_u32(ring + (size_t)st * STAGE);
-                        const uint64_t da = desc_k(sa), db = desc_k(sa + kABytes);
+                        const uint64_t da = desc_k(FEW ? sa : sa + WEIGHTS), db = desc_k(FEW ? sa + WEIGHTS : sa);
     #pragma unroll
                         for (int k = 0; k < 4; k++)
-                            mma_e4m3<1>(tmem + (uint32_t)(buf * NF), da + 2 * k, db + 2 * k, id, k > 0);
+                            mma_e4m3<1>(tmem + (uint32_t)(buf * CFG::COLS), da + 2 * k, db + 2 * k, id, k > 0);
                         commit<1>(smem_u32(&empty[st]));
                         commit<1>(smem_u32(&acc_full[buf]));
                         if (++st == a.stages) { st = 0; ph ^= 1; }
@@ -204,23 +226,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else {
-        if (SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        // ============ sums: rows 32 q + lane, columns c0 .. c0 + CW - 1
+        if (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        // ============ sums.  MANY: rows 32 q + lane, CW features from c0 on; FEW: feature
+        // 32 q + lane, every row
         const int q = warp & 3, c0 = CW * ((warp - 4) >> 2), nb = (a.M + 127) / 128;
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
         while (ok && tiles.next(v)) {
-            const int m0 = v.m * NF + c0;                      // the warp's first feature
-            const bool works = 32 * q < v.n && m0 < a.M;   // the warp has rows and features
-            const bool mine = works && 32 * q + lane < v.n;
-            const float* xsp = a.xs + v.r0 + 32 * q + lane;
+            const int m0 = v.m * NF + (FEW ? 32 * q : c0);            // the warp's first feature
+            const bool works = m0 < a.M && (FEW || 32 * q < v.n);     // the warp has features and rows
+            const int row = FEW ? lane : 32 * q + lane;               // whose scales the lane fetches
+            const bool scales = works && row < v.n;
+            const float* xsp = a.xs + v.r0 + row;
             const float* wsp = a.ws + ((int64_t)v.e * nb + m0 / 128) * a.blocks;
             float acc[CW], xs[GROUP], ws[GROUP];
             auto fetch = [&](int b0) {
 #pragma unroll
                 for (int g = 0; g < GROUP; g++) {
-                    const bool in = mine && b0 + g < a.blocks;
+                    const bool in = scales && b0 + g < a.blocks;
                     xs[g] = fetch_f32(xsp + (int64_t)(b0 + g) * a.rows, in);
                     ws[g] = fetch_f32(wsp + b0 + g, in);
                 }
@@ -231,7 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b0 = 0; ok && b0 < a.blocks; b0 += GROUP) {
                 float s[GROUP];
 #pragma unroll
-                for (int g = 0; g < GROUP; g++) s[g] = xs[g] * ws[g];
+                for (int g = 0; g < GROUP; g++) {
+                    s[g] = xs[g] * ws[g];
+                    if (FEW) s_scale[warp - 4][g][lane] = s[g];   // of all rows, for all lanes
+                }
+                if (FEW) __syncwarp();
                 fetch(b0 + GROUP);
 #pragma unroll
                 for (int g = 0; g < GROUP; g++) {
@@ -239,16 +267,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort_v, a.wait, err))) break;
                     fence_after();
                     if (works) {
-                        const uint32_t src = tmem + (uint32_t)(buf * NF + c0) + ((uint32_t)(32 * q) << 16);
-                        uint32_t d[2][16];   // 16 columns on their way while 16 are added
-                        tmem_ld16(src, d[0]);
+                        const uint32_t src = tmem + (uint32_t)(buf * CFG::COLS + (FEW ? 0 : c0)) + ((uint32_t)(32 * q) << 16);
+                        if constexpr (FEW) {
 #pragma unroll
-                        for (int c = 0; c < CW; c += 16) {
-                            wait_ld(d[(c / 16) & 1]);
-                            if (c + 16 < CW) tmem_ld16(src + c + 16, d[(c / 16 + 1) & 1]);
+                            for (int c = 0; c < CW; c += 16) {
+                                if (c >= v.n) break;
+                                uint32_t d[16];
+                                tmem_ld16(src + c, d);
+                                wait_ld(d);
 #pragma unroll
-                            for (int j = 0; j < 16; j++)
-                                acc[c + j] = fmaf(__uint_as_float(d[(c / 16) & 1][j]), s[g], acc[c + j]);
+                                for (int j = 0; j < 16; j += 4) {
+                                    const float4 t = *reinterpret_cast<const float4*>(&s_scale[warp - 4][g][c + j]);
+                                    acc[c + j] = fmaf(__uint_as_float(d[j]), t.x, acc[c + j]);
+                                    acc[c + j + 1] = fmaf(__uint_as_float(d[j + 1]), t.y, acc[c + j + 1]);
+                                    acc[c + j + 2] = fmaf(__uint_as_float(d[j + 2]), t.z, acc[c + j + 2]);
+                                    acc[c + j + 3] = fmaf(__uint_as_float(d[j + 3]), t.w, acc[c + j + 3]);
+                                }
+                            }
+                        } else {
+                            uint32_t d[2][16];   // 16 columns on their way while 16 are added
+                            tmem_ld16(src, d[0]);
+#pragma unroll
+                            for (int c = 0; c < CW; c += 16) {
+                                wait_ld(d[(c / 16) & 1]);
+                                if (c + 16 < CW) tmem_ld16(src + c + 16, d[(c / 16 + 1) & 1]);
+#pragma unroll
+                                for (int j = 0; j < 16; j++)
+                                    acc[c + j] = fmaf(__uint_as_float(d[(c / 16) & 1][j]), s[g], acc[c + j]);
+                            }
                         }
                     }
                     fence_before();
@@ -258,8 +304,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            if (mine) {
-                const int64_t at = (int64_t)(v.r0 + 32 * q + lane) * a.ldo + m0;
+            if (FEW) {
+                if (m0 + lane < a.M) {
+                    const int64_t at = (int64_t)v.r0 * a.ldo + m0 + lane;
+                    float* of = static_cast<float*>(a.out) + at;
+                    uint16_t* oh = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+                    for (int c = 0; c < CW; c++)
+                        if (c < v.n) {
+                            if (a.out_f32) of[c * a.ldo] = acc[c];
+                            else oh[c * a.ldo] = f32_to_bf16_bits(acc[c]);
+                        }
+                }
+            } else if (scales) {
+                const int64_t at = (int64_t)(v.r0 + row) * a.ldo + m0;
                 const int n = min(CW, a.M - m0);   // a multiple of 8
                 if (a.out_f32) {
                     float* o = static_cast<float*>(a.out) + at;
@@ -291,32 +349,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         fence_after();
-        tmem_dealloc<1>(tmem, 512);
+        tmem_dealloc<1>(tmem, TMEM);
     }
 }
 
-template <int NF>
-int launch(Args& a, const RowMaps& ta, const CUtensorMap& tb, cudaStream_t st)
+template <class CFG>
+int launch(Args& a, const RowMaps& tr, const CUtensorMap& tw, cudaStream_t st)
 {
-    constexpr int STAGE = kABytes + NF * 128;
     static std::atomic<int> smem_set[kMaxDevices];
-    auto* kern = gg8_kernel<NF>;
+    auto* kern = gg8_kernel<CFG>;
     int sms = 0;
-    if (int rc = prepare_launch(kern, smem_set, &sms)) return rc;
+    if (int rc = prepare_launch(kern, kSmemMax - kStatic, smem_set, &sms)) return rc;
     const int fixed = plan_bytes(a.E);
-    a.stages = (kSmemMax - 1024 - fixed) / STAGE;   // 1 KB static
+    a.stages = (kSmemMax - kStatic - fixed) / CFG::STAGE;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    const int smem = fixed + a.stages * STAGE;
-    if (NF == 256) {   // the register split counts on what the kernel was compiled to
+    const int smem = fixed + a.stages * CFG::STAGE;
+    if (!CFG::FEW) {   // the register split counts on what the kernel was compiled to
         static const int regs = [] {
             cudaFuncAttributes at{};
-            return cudaFuncGetAttributes(&at, gg8_kernel<NF>) == cudaSuccess ? at.numRegs : 0;
+            return cudaFuncGetAttributes(&at, gg8_kernel<CFG>) == cudaSuccess ? at.numRegs : 0;
         }();
         if (regs != kRegs) return MOE_ERR_UNSUPPORTED;
     }
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    MOE_CUDA_TRY(launch_clusters(kern, sms, 1, kThreads, smem, st, ta, tb, a));
+    MOE_CUDA_TRY(launch_clusters(kern, sms, 1, CFG::THREADS, smem, st, tr, tw, a));
     return MOE_OK;
 }
 
@@ -362,17 +419,16 @@ extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, co
     a.blocks = (in + 127) / 128;
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
-    // 128 features a tile while the call streams weights for few rows: more
-    // tiles to spread over the SMs
     const bool few = rows <= 16 * (int64_t)experts;
     a.box = few ? 16 : 32;
-    RowMaps ta;
-    CUtensorMap tb;
+    RowMaps tr;
+    CUtensorMap tw;
     const uint64_t wd[3] = {(uint64_t)in, (uint64_t)out, (uint64_t)experts};
     const uint64_t wst[2] = {(uint64_t)in, (uint64_t)in * out};
     const uint32_t wb[3] = {128, few ? 128u : 256u, 1};
-    if (!encode_rows(&ta, E_U8, d_xq, ldxq, in, rows, a.box, 128) || !encode_map(&tb, E_U8, 3, d_wq, wd, wst, wb))
+    if (!encode_rows(&tr, E_U8, d_xq, ldxq, in, rows, a.box, few ? 32 : 128) ||
+        !encode_map(&tw, E_U8, 3, d_wq, wd, wst, wb))
         return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return few ? launch<128>(a, ta, tb, st) : launch<256>(a, ta, tb, st);
+    return few ? launch<Cfg<true>>(a, tr, tw, st) : launch<Cfg<false>>(a, tr, tw, st);
 }

@@ -165,8 +165,8 @@ struct CopyPos {
     uint32_t ph;
 };
 // A copy warp's loop over the stages of its tiles, walked by one thread:
-// next() gives the steps of the next tile or -1, issue(s, bar, stage) starts
-// the copies of step s and announces their bytes on the stage's barrier.
+// next() gives the steps of the next tile or -1, issue(s, bar, address, stage)
+// starts the copies of step s and announces their bytes on the stage's barrier.
 // `withheld`: the first stage is never filled (a test's doing).
 template <int STAGE, class NEXT, class ISSUE>
 __device__ __forceinline__ void copy_loop(uint64_t* full, uint64_t* empty, unsigned char* ring, int stages,
@@ -181,7 +181,7 @@ __device__ __forceinline__ void copy_loop(uint64_t* full, uint64_t* empty, unsig
         for (int s = 0; s < steps; s++) {
             if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_flag, limit, error))) break;
             if (withheld) withheld = false;
-            else issue(s, smem_u32(&full[st]), smem_u32(ring) + (uint32_t)(st * STAGE));
+            else issue(s, smem_u32(&full[st]), smem_u32(ring) + (uint32_t)(st * STAGE), st);
             issued++;
             if (++st == stages) { st = 0; ph ^= 1; }
         }
@@ -530,9 +530,10 @@ static inline bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_B
 static inline int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
 
 // SMs of the current device.  The first launch of a kernel on a device also
-// lets it use all of an SM's shared memory (`smem_set`: one flag a device).
+// lets it use `most` bytes of dynamic shared memory (`smem_set`: one flag a
+// device).
 template <class K>
-static inline int prepare_launch(K* kern, std::atomic<int>* smem_set, int* sms)
+static inline int prepare_launch(K* kern, int most, std::atomic<int>* smem_set, int* sms)
 {
     static std::atomic<int> count[kMaxDevices];
     int dev = 0;
@@ -543,7 +544,7 @@ static inline int prepare_launch(K* kern, std::atomic<int>* smem_set, int* sms)
         count[dev].store(*sms, std::memory_order_relaxed);
     }
     if (!smem_set[dev].load(std::memory_order_relaxed)) {
-        MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 1024));
+        MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         smem_set[dev].store(1, std::memory_order_relaxed);
     }
     return MOE_OK;

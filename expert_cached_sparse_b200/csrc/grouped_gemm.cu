@@ -43,7 +43,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
 constexpr int kMaxStages = 12;
 constexpr int kStatic = 1024;        // bytes of static shared memory at most
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
@@ -52,9 +51,16 @@ constexpr int kStaging = 4 * 2 * 4096;
 // Steps of 64 summed in one accumulator where the output is float32.  The
 // tensor core adds to its fp32 accumulator with truncation, so the relative
 // error of a sum grows by about 1e-6 for every 1000 inner indices; partial
-// sums of 512 are added to the output, rounded to nearest.  (bf16 outputs
-// round to 2^-9 anyway: one accumulator for the whole sum.)
+// sums of 512 are added up outside it, rounded to nearest: in registers (FWD,
+// DX: adding them to the output took 474 us instead of 208 where a tile has
+// eight of them) or in the output (DW: few experts have several).  bf16
+// outputs round to 2^-9 anyway: one accumulator for the whole sum.
 constexpr int kPartial = 8;
+
+// Registers a thread of the control warps and of the epilogue's where the
+// latter hold 128 float32 sums each: together what the block is launched with,
+// 128 * 72 + 256 * 216 = 384 * 168.
+constexpr int kRegs = 168, kControlRegs = 72, kSumRegs = 216;
 
 enum Mode { FWD, DX, DW };
 
@@ -147,17 +153,9 @@ struct Units<DW, NB, 1> {
     }
 };
 
-__device__ __forceinline__ void put(float* p, uint32_t d, bool add)
-{
-    const float x = __uint_as_float(d);
-    *p = add ? *p + x : x;
-}
-__device__ __forceinline__ void put(uint16_t* p, uint32_t d, bool) { *p = f32_to_bf16_bits(__uint_as_float(d)); }
-
 // A warp's 32 features of n columns, ldo elements apart: each store is 32
 // adjacent elements of one column.  `mine`: whether the lane's feature exists.
-template <class T>
-__device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int n, bool mine, bool add)
+__device__ __forceinline__ void store_cols(uint16_t* p, int64_t ldo, uint32_t src, int n, bool mine)
 {
     for (int c = 0; c < n; c += 16) {
         uint32_t d[16];
@@ -166,7 +164,7 @@ __device__ __forceinline__ void store_cols(T* p, int64_t ldo, uint32_t src, int 
         if (mine) {
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-                if (c + j < n) put(p, d[j], add);
+                if (c + j < n) *p = f32_to_bf16_bits(__uint_as_float(d[j]));
                 p += ldo;
             }
         }
@@ -246,8 +244,18 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap& out
     }
 }
 
-template <int MODE, int NB, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+// SUMS: float32 outputs of row products, summed up in the epilogue's registers.
+template <int NB, bool SUMS>
+struct Epilogue {
+    static constexpr int WARPS = SUMS && NB > 32 ? 8 : 4;
+    static constexpr int THREADS = 128 + 32 * WARPS;
+    static constexpr int CW = NB / (WARPS / 4);        // columns of one warp
+    static constexpr bool SPLIT = SUMS && CW > 64;     // registers moved from the control warps
+};
+static_assert(128 * kControlRegs + 256 * kSumRegs <= 384 * kRegs, "a larger split never starts");
+
+template <int MODE, int NB, int CG, bool SUMS>
+__global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
     gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
               const __grid_constant__ CUtensorMap tm_out, const Args a)
 {
@@ -255,12 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t TMEM = 2 * NB;
     constexpr bool RELAY = MODE == DW || CG == 2;
     constexpr bool PAIR = CG == 2;
+    using EPI = Epilogue<NB, SUMS>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
     __shared__ uint32_t s_tmem;
     __shared__ CopyPos s_copy[2];
     __shared__ int s_abort, s_live;
-    __shared__ long long s_scan[4];
+    __shared__ long long s_scan[EPI::WARPS];
     unsigned char* ring = smem_raw;
     unsigned char* staging = ring + (size_t)a.stages * STAGE;   // DW: 4 warps x 2 tiles of 32 rows x 128 bytes
     PlanExpert* tab = reinterpret_cast<PlanExpert*>(staging + (MODE == DW ? kStaging : 0));
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), 4 * CG);
+            mbar_init(smem_u32(&acc_empty[i]), EPI::WARPS * CG);
         }
         mbar_init(smem_u32(&fin), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (MODE == DW)
             for (int i = tid - 128; i <= a.E; i += 128) off[i] = __ldg(a.offsets + i);
         else
-            build_plan<128>(a.offsets, a.E, a.rows, {NB}, tab, s_scan, &s_live);
+            build_plan<32 * EPI::WARPS>(a.offsets, a.E, a.rows, {NB}, tab, s_scan, &s_live);
     }
     fence_before();
     __syncthreads();
@@ -308,134 +317,139 @@ __global__ void __launch_bounds__(kThreads, 1)
     Units<MODE, NB, CG> units(a, tab, off, MODE == DW ? 0 : s_live, rank);
     Unit v;
 
-    if (warp == 0) {
-        // ============ copies of the features (A)
-        if (elect1())
-            copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
-                             [&] { return units.next(v) ? v.steps : -1; },
-                             [&](int s, uint32_t bar, uint32_t sa, int) {
-                                 const int k = v.k0 + 64 * s;
-                                 mbar_expect_tx(bar, kABytes);
-                                 if (MODE == FWD) {
-                                     tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
-                                 } else if (a.chunks_a) {
-                                     if (MODE == DX) tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
-                                     else tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
-                                 } else
-                                     for (int i = 0; i < 2; i++) {
-                                         if (MODE == DX) tma_3d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, v.e, bar);
-                                         else tma_2d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, bar);
-                                     }
-                             });
-        __syncwarp();
-        drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
-    } else if (warp == 2) {
-        // ============ copies of the columns (B)
-        if (elect1()) {
-            int ub = 0;
-            uint32_t bytes = 0;
-            copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
-                             [&] {
-                                 if (!units.next(v)) return -1;
-                                 ub = MODE == DW ? (a.chunks_b ? NB / 64 : (v.n + 63) / 64) : row_units(v.nb, a.box);
-                                 bytes = (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
-                                 return v.steps;
-                             },
-                             [&](int s, uint32_t bar, uint32_t sa, int) {
-                                 const int k = v.k0 + 64 * s;
-                                 const uint32_t sb = sa + kABytes;
-                                 if (PAIR && bytes == 0) {   // a pair's second half without columns
-                                     mbar_arrive(bar);
-                                     return;
-                                 }
-                                 mbar_expect_tx(bar, bytes);
-                                 if (MODE != DW)
-                                     tma_rows(sb, tm_b, k, v.cb, ub, a.box, bar);
-                                 else if (a.chunks_b)
-                                     tma_3d(sb, &tm_b.m[0], 0, k, v.cb / 64, bar);
-                                 else
-                                     for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.cb + 64 * i, k, bar);
-                             });
-        }
-        __syncwarp();
-        drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
-    } else if (warp == 1) {
-        // ============ MMAs
-        if (rank == 0) {
+    if (warp < 4) {
+        if (EPI::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (warp == 0) {
+            // ============ copies of the features (A)
+            if (elect1())
+                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
+                                 [&] { return units.next(v) ? v.steps : -1; },
+                                 [&](int s, uint32_t bar, uint32_t sa, int) {
+                                     const int k = v.k0 + 64 * s;
+                                     mbar_expect_tx(bar, kABytes);
+                                     if (MODE == FWD) {
+                                         tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
+                                     } else if (a.chunks_a) {
+                                         if (MODE == DX) tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
+                                         else tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
+                                     } else
+                                         for (int i = 0; i < 2; i++) {
+                                             if (MODE == DX) tma_3d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, v.e, bar);
+                                             else tma_2d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, bar);
+                                         }
+                                 });
+            __syncwarp();
+            drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
+        } else if (warp == 2) {
+            // ============ copies of the columns (B)
             if (elect1()) {
-                int st = 0, it = 0;
+                int ub = 0;
+                uint32_t bytes = 0;
+                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
+                                 [&] {
+                                     if (!units.next(v)) return -1;
+                                     ub = MODE == DW ? (a.chunks_b ? NB / 64 : (v.n + 63) / 64) : row_units(v.nb, a.box);
+                                     bytes = (uint32_t)(ub * (MODE == DW ? 8192 : a.box * 128));
+                                     return v.steps;
+                                 },
+                                 [&](int s, uint32_t bar, uint32_t sa, int) {
+                                     const int k = v.k0 + 64 * s;
+                                     const uint32_t sb = sa + kABytes;
+                                     if (PAIR && bytes == 0) {   // a pair's second half without columns
+                                         mbar_arrive(bar);
+                                         return;
+                                     }
+                                     mbar_expect_tx(bar, bytes);
+                                     if (MODE != DW)
+                                         tma_rows(sb, tm_b, k, v.cb, ub, a.box, bar);
+                                     else if (a.chunks_b)
+                                         tma_3d(sb, &tm_b.m[0], 0, k, v.cb / 64, bar);
+                                     else
+                                         for (int i = 0; i < ub; i++) tma_2d(sb + 8192 * i, &tm_b.m[0], v.cb + 64 * i, k, bar);
+                                 });
+            }
+            __syncwarp();
+            drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
+        } else if (warp == 1) {
+            // ============ MMAs
+            if (rank == 0) {
+                if (elect1()) {
+                    int st = 0, it = 0;
+                    uint32_t ph = 0;
+                    bool ok = true;
+                    while (ok && units.next(v)) {
+                        const uint32_t id = idesc_bf16<CG>(CG * v.nh, MODE != FWD, MODE == DW);
+                        uint32_t d = 0;
+                        int left = 0;   // steps until the accumulator changes
+                        for (int s = 0; s < v.steps; s++) {
+                            const bool first = left == 0;
+                            if (first) {
+                                const int ab = it & 1;
+                                if (it >= 2 &&   // the epilogue has read what this accumulator held
+                                    !(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
+                                    break;
+                                d = tmem + (uint32_t)(ab * NB);
+                                left = min(a.partial, v.steps - s);
+                            }
+                            const uint32_t bar = smem_u32(RELAY ? &ready[st] : &full[st]);
+                            if (!(ok = mbar_wait(bar, ph, abort_v, a.wait, err))) break;
+                            fence_after();
+                            const uint32_t sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
+                            const uint64_t da = MODE == FWD ? desc_k(sa) : desc_mn(sa, 8192);
+                            const uint64_t db = MODE == DW ? desc_mn(sb, 8192) : desc_k(sb);
+                            // 16 inner indices: 32 bytes along a K-major row, 16 rows MN-major
+                            const int kk = MODE == DW && s == v.steps - 1 ? (v.tail + 15) / 16 : 4;
+    #pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                if (MODE != DW || k < kk)
+                                    mma_bf16<CG>(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id,
+                                                 !first || k > 0);
+                            commit<CG>(smem_u32(&empty[st]));   // the stage is free once these MMAs have read it
+                            if (++st == a.stages) { st = 0; ph ^= 1; }
+                            if (--left == 0) {
+                                commit<CG>(smem_u32(&acc_full[it & 1]));
+                                it++;
+                            }
+                        }
+                    }
+                    commit<CG>(smem_u32(&fin));   // every MMA completes before tensor memory is released
+                    mbar_drain(smem_u32(&fin), 0, err);
+                }
+                __syncwarp();
+            }
+        } else if (warp == 3) {
+            // ============ between copies and MMAs
+            if (RELAY) {
+                int st = 0;
                 uint32_t ph = 0;
                 bool ok = true;
                 while (ok && units.next(v)) {
-                    const uint32_t id = idesc_bf16<CG>(CG * v.nh, MODE != FWD, MODE == DW);
-                    uint32_t d = 0;
-                    int left = 0;   // steps until the accumulator changes
                     for (int s = 0; s < v.steps; s++) {
-                        const bool first = left == 0;
-                        if (first) {
-                            const int ab = it & 1;
-                            if (it >= 2 &&   // the epilogue has read what this accumulator held
-                                !(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
-                                break;
-                            d = tmem + (uint32_t)(ab * NB);
-                            left = min(a.partial, v.steps - s);
+                        if (!(ok = mbar_wait_warp(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
+                        if (MODE == DW && s == v.steps - 1 && (v.tail & 15)) {
+                            // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
+                            unsigned char* p = ring + (size_t)st * STAGE + 128 * v.tail;
+                            const int z = 128 * (16 - (v.tail & 15)), chunks = 2 + (v.nh + 63) / 64;
+                            for (int i = 16 * lane; i < z; i += 512)
+                                for (int c = 0; c < chunks; c++)
+                                    *reinterpret_cast<uint4*>(p + 8192 * c + i) = make_uint4(0, 0, 0, 0);
+                            asm volatile("fence.proxy.async;" ::: "memory");
+                            if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                            __syncwarp();
                         }
-                        const uint32_t bar = smem_u32(RELAY ? &ready[st] : &full[st]);
-                        if (!(ok = mbar_wait(bar, ph, abort_v, a.wait, err))) break;
-                        fence_after();
-                        const uint32_t sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
-                        const uint64_t da = MODE == FWD ? desc_k(sa) : desc_mn(sa, 8192);
-                        const uint64_t db = MODE == DW ? desc_mn(sb, 8192) : desc_k(sb);
-                        // 16 inner indices: 32 bytes along a K-major row, 16 rows MN-major
-                        const int kk = MODE == DW && s == v.steps - 1 ? (v.tail + 15) / 16 : 4;
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            if (MODE != DW || k < kk)
-                                mma_bf16<CG>(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id,
-                                             !first || k > 0);
-                        commit<CG>(smem_u32(&empty[st]));   // the stage is free once these MMAs have read it
+                        if (lane == 0) {
+                            if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&ready[st]), 0));
+                            else mbar_arrive(smem_u32(&ready[st]));
+                        }
                         if (++st == a.stages) { st = 0; ph ^= 1; }
-                        if (--left == 0) {
-                            commit<CG>(smem_u32(&acc_full[it & 1]));
-                            it++;
-                        }
                     }
-                }
-                commit<CG>(smem_u32(&fin));   // every MMA completes before tensor memory is released
-                mbar_drain(smem_u32(&fin), 0, err);
-            }
-            __syncwarp();
-        }
-    } else if (warp == 3) {
-        // ============ between copies and MMAs
-        if (RELAY) {
-            int st = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            while (ok && units.next(v)) {
-                for (int s = 0; s < v.steps; s++) {
-                    if (!(ok = mbar_wait_warp(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
-                    if (MODE == DW && s == v.steps - 1 && (v.tail & 15)) {
-                        // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
-                        unsigned char* p = ring + (size_t)st * STAGE + 128 * v.tail;
-                        const int z = 128 * (16 - (v.tail & 15)), chunks = 2 + (v.nh + 63) / 64;
-                        for (int i = 16 * lane; i < z; i += 512)
-                            for (int c = 0; c < chunks; c++)
-                                *reinterpret_cast<uint4*>(p + 8192 * c + i) = make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async;" ::: "memory");
-                        if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&ready[st]), 0));
-                        else mbar_arrive(smem_u32(&ready[st]));
-                    }
-                    if (++st == a.stages) { st = 0; ph ^= 1; }
                 }
             }
         }
     } else {
-        // ============ epilogue: lane quarter q = warp % 4, one feature per thread
+        if (EPI::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        // ============ epilogue: lane quarter q = warp % 4, one feature per thread; SUMS: columns
+        // from cw on, CW of them
         const int q = warp & 3;
         int it = 0, turn = 0;
         bool ok = true;
@@ -444,6 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = f < a.M;
             const bool none = MODE == DW && v.steps == 0;   // an expert without rows: its gradient is zero
             if (none && a.accumulate) continue;
+            const int cw = EPI::CW * ((warp - 4) >> 2);
+            float sum[SUMS ? EPI::CW : 1];
+            if (SUMS) {
+#pragma unroll
+                for (int c = 0; c < EPI::CW; c++) sum[c] = 0.0f;
+            }
             // one accumulator, or the partial sums of every a.partial steps
             for (int s = 0; s == 0 || s < v.steps; s += a.partial) {
                 const int ab = it & 1;
@@ -468,10 +488,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (s > 0 && lane == 0) bulk_wait();   // the partial sums before are in place
                         store_tile(a, tm_out, v, staging + 8192 * q, turn, src, v.m0 + 32 * q, none, add);
                     }
-                } else if (a.out_f32) {
-                    store_cols(static_cast<float*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine, add);
+                } else if constexpr (SUMS) {
+#pragma unroll
+                    for (int c = 0; c < EPI::CW; c += 16) {
+                        if (cw + c >= v.n) break;
+                        uint32_t d[16];
+                        tmem_ld16(src + cw + c, d);
+                        wait_ld(d);
+#pragma unroll
+                        for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(d[j]);
+                    }
                 } else {
-                    store_cols(static_cast<uint16_t*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine, false);
+                    store_cols(static_cast<uint16_t*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
                 }
                 if (none) break;
                 fence_before();
@@ -481,6 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else mbar_arrive(smem_u32(&acc_empty[ab]));
                 }
                 it++;
+            }
+            if (SUMS && ok) {
+                float* o = static_cast<float*>(a.out) + (int64_t)(v.c0 + cw) * a.ldo + f;
+#pragma unroll
+                for (int c = 0; c < EPI::CW; c++)
+                    if (mine && cw + c < v.n) o[c * a.ldo] = sum[c];
+                __syncwarp();
             }
         }
         if (MODE == DW && lane == 0) bulk_wait();   // the staging tiles are read, the stores done
@@ -495,21 +530,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PAIR) cluster_sync();
 }
 
-template <int MODE, int NB, int CG>
-int launch_nb(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, cudaStream_t st)
+template <int MODE, int NB, int CG, bool SUMS>
+int launch(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NB / CG * 128;
+    using EPI = Epilogue<NB, SUMS>;
     static std::atomic<int> smem_set[kMaxDevices];
-    auto* kern = gg_kernel<MODE, NB, CG>;
+    auto* kern = gg_kernel<MODE, NB, CG, SUMS>;
     int sms = 0;
     if (int rc = prepare_launch(kern, kSmemMax - kStatic, smem_set, &sms)) return rc;
     const int fixed = MODE == DW ? kStaging + (int)align_up(4 * (a.E + 1), 128) : plan_bytes(a.E);
     a.stages = (kSmemMax - kStatic - fixed) / STAGE;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = fixed + a.stages * STAGE;
+    if (EPI::SPLIT) {   // the register split counts on what the kernel was compiled to
+        static const int regs = [] {
+            cudaFuncAttributes at{};
+            return cudaFuncGetAttributes(&at, gg_kernel<MODE, NB, CG, SUMS>) == cudaSuccess ? at.numRegs : 0;
+        }();
+        if (regs != kRegs) return MOE_ERR_UNSUPPORTED;
+    }
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    MOE_CUDA_TRY(launch_clusters(kern, sms, CG, kThreads, smem, st, ta, tb, to, a));
+    MOE_CUDA_TRY(launch_clusters(kern, sms, CG, EPI::THREADS, smem, st, ta, tb, to, a));
     return MOE_OK;
 }
 
@@ -563,7 +606,8 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     a.box = small ? 16 : 32;
     if (!encode_rows(&tb, E_BF16, x, ldx, a.K, rows, a.box, small ? 32 : 128)) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return small ? launch_nb<MODE, 32, 1>(a, ta, tb, ta, st) : launch_nb<MODE, 256, 2>(a, ta, tb, ta, st);
+    if (a.out_f32) return small ? launch<MODE, 32, 1, true>(a, ta, tb, ta, st) : launch<MODE, 256, 2, true>(a, ta, tb, ta, st);
+    return small ? launch<MODE, 32, 1, false>(a, ta, tb, ta, st) : launch<MODE, 256, 2, false>(a, ta, tb, ta, st);
 }
 
 }  // namespace
@@ -682,5 +726,5 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
         !encode_map(&to, a.out_f32 ? E_F32 : E_BF16, 3, d_dw, dims, strides, box))
         return MOE_ERR_CUDA;
     a.box = 256;   // one map of the columns
-    return launch_nb<DW, 256, 1>(a, ta, tb, to, st);
+    return launch<DW, 256, 1, false>(a, ta, tb, to, st);
 }

@@ -75,6 +75,7 @@ struct Args {
     int K;           // inner size (DW: ragged)
     int stages;
     int partial;     // steps summed in one accumulator
+    int split;       // CTAs of a cluster that share a tile's inner index
     int box;         // smallest height of a copy of the ragged operand (FWD, DX)
     int chunks_a, chunks_b;   // whether one copy brings all 64-column chunks of an MN-major operand
     long long wait;  // limit of every bounded wait, in SM clock cycles
@@ -95,9 +96,14 @@ struct Units {
     PlanWalk walk;
     const int rank;
 
+    int split, s0, s1;   // CG = 1: the cluster's CTAs that share the inner index, this one's steps
+
     __device__ Units(const Args& a_, const PlanExpert* tab, const int*, int live, int rank_)
-        : a(a_), walk(tab, live, {NB}, (a_.M + 128 * CG - 1) / (128 * CG), blockIdx.x / CG, gridDim.x / CG), rank(rank_)
+        : a(a_), walk(tab, live, {NB}, (a_.M + 128 * CG - 1) / (128 * CG), blockIdx.x / (CG * a_.split),
+                      gridDim.x / (CG * a_.split)),
+          rank(CG == 2 ? rank_ : 0), split(a_.split)
     {
+        walk.split_steps((a.K + 63) / 64, rank_, split, s0, s1);
     }
     __device__ __forceinline__ bool next(Unit& v)
     {
@@ -107,8 +113,8 @@ struct Units {
         v.m0 = (w.m * CG + rank) * 128;
         v.c0 = w.r0;
         v.n = w.n;
-        v.k0 = 0;
-        v.steps = (a.K + 63) / 64;
+        v.k0 = 64 * s0;
+        v.steps = s1 - s0;
         v.tail = 64;
         v.nh = mma_rows<CG>(v.n) / CG;
         v.cb = v.c0 + v.nh * rank;
@@ -123,6 +129,7 @@ template <int NB>
 struct Units<DW, NB, 1> {
     const Args& a;
     const int* off;   // the offsets, in shared memory
+    static constexpr int split = 1;
     const int mt, per;
     long long u, total;
 
@@ -244,7 +251,8 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap& out
     }
 }
 
-// SUMS: float32 outputs of row products, summed up in the epilogue's registers.
+// SUMS: row products summed up in the epilogue's registers, for float32 outputs
+// and for an inner index split over a cluster.
 template <int NB, bool SUMS>
 struct Epilogue {
     static constexpr int WARPS = SUMS && NB > 32 ? 8 : 4;
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
     PlanExpert* tab = reinterpret_cast<PlanExpert*>(staging + (MODE == DW ? kStaging : 0));
     int* off = reinterpret_cast<int*>(tab);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int rank = MODE == DW ? 0 : (int)cluster_rank();   // of a pair, or of a cluster that splits the inner index
     volatile int* abort_v = &s_abort;
     int* err = &g_gemm_error;
 
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
             drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 1) {
             // ============ MMAs
-            if (rank == 0) {
+            if (!PAIR || rank == 0) {
                 if (elect1()) {
                     int st = 0, it = 0;
                     uint32_t ph = 0;
@@ -446,13 +454,14 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                 }
             }
         }
+        if (SUMS && units.split > 1) split_others();
     } else {
         if (EPI::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // ============ epilogue: lane quarter q = warp % 4, one feature per thread; SUMS: columns
         // from cw on, CW of them
         const int q = warp & 3;
         int it = 0, turn = 0;
-        bool ok = true;
+        bool ok = true, reduced = false;
         while (ok && units.next(v)) {
             const int f = v.m0 + 32 * q + lane;
             const bool mine = f < a.M;
@@ -510,14 +519,30 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                 }
                 it++;
             }
-            if (SUMS && ok) {
-                float* o = static_cast<float*>(a.out) + (int64_t)(v.c0 + cw) * a.ldo + f;
+            if constexpr (SUMS) {
+                if (!ok) break;
+                if (units.split > 1) {
+                    if constexpr (CG == 1) split_reduce(sum, ring, rank, units.split, 32 * q + lane);
+                    reduced = true;
+                    if (rank) break;
+                }
+                const int64_t at = (int64_t)(v.c0 + cw) * a.ldo + f;
+                const int n = mine ? v.n - cw : 0;
+                if (a.out_f32) {
+                    float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
-                for (int c = 0; c < EPI::CW; c++)
-                    if (mine && cw + c < v.n) o[c * a.ldo] = sum[c];
+                    for (int c = 0; c < EPI::CW; c++, o += a.ldo)
+                        if (c < n) *o = sum[c];
+                } else {
+                    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+                    for (int c = 0; c < EPI::CW; c++, o += a.ldo)
+                        if (c < n) *o = f32_to_bf16_bits(sum[c]);
+                }
                 __syncwarp();
             }
         }
+        if (SUMS && units.split > 1 && !reduced) split_others();   // no tile, or a wait that ran out
         if (MODE == DW && lane == 0) bulk_wait();   // the staging tiles are read, the stores done
     }
     fence_before();
@@ -531,14 +556,14 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
 }
 
 template <int MODE, int NB, int CG, bool SUMS>
-int launch(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, cudaStream_t st)
+int launch(Args& a, int64_t tiles, int sms, int dev, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to,
+           cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NB / CG * 128;
     using EPI = Epilogue<NB, SUMS>;
     static std::atomic<int> smem_set[kMaxDevices];
     auto* kern = gg_kernel<MODE, NB, CG, SUMS>;
-    int sms = 0;
-    if (int rc = prepare_launch(kern, kSmemMax - kStatic, smem_set, &sms)) return rc;
+    if (int rc = allow_smem(kern, kSmemMax - kStatic, smem_set, dev)) return rc;
     const int fixed = MODE == DW ? kStaging + (int)align_up(4 * (a.E + 1), 128) : plan_bytes(a.E);
     a.stages = (kSmemMax - kStatic - fixed) / STAGE;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
@@ -552,7 +577,7 @@ int launch(Args& a, const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap&
     }
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    MOE_CUDA_TRY(launch_clusters(kern, sms, CG, EPI::THREADS, smem, st, ta, tb, to, a));
+    MOE_CUDA_TRY(launch_clusters(kern, sms, tiles, CG * a.split, EPI::THREADS, smem, st, ta, tb, to, a));
     return MOE_OK;
 }
 
@@ -602,12 +627,24 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     } else if (!map_mn(&ta, &a.chunks_a, w, in, in, out, 2, E)) {
         return MOE_ERR_CUDA;
     }
-    const bool small = rows <= 16 * (int64_t)E;
+    int sms = 0, dev = 0;
+    if (int rc = device_sms(&sms, &dev)) return rc;
+    // Tiles of 32 rows where the experts have few (each tile streams its
+    // weights whatever its rows: 243 us against 265 with tiles of 256 for 16
+    // tokens x 6 of 256 experts), or where so many still fit the SMs at once;
+    // pairs of CTAs and 256 rows else (4096 tokens: 1.5 ms against 4).
+    const int64_t small_tiles = most_tiles(E, rows, 32, (a.M + 127) / 128);
+    const bool small = rows <= 16 * (int64_t)E || small_tiles <= sms;
     a.box = small ? 16 : 32;
     if (!encode_rows(&tb, E_BF16, x, ldx, a.K, rows, a.box, small ? 32 : 128)) return MOE_ERR_CUDA;
+    a.split = small ? split_of(small_tiles, (a.K + 63) / 64, sms) : 1;
     cudaStream_t st = as_stream(stream);
-    if (a.out_f32) return small ? launch<MODE, 32, 1, true>(a, ta, tb, ta, st) : launch<MODE, 256, 2, true>(a, ta, tb, ta, st);
-    return small ? launch<MODE, 32, 1, false>(a, ta, tb, ta, st) : launch<MODE, 256, 2, false>(a, ta, tb, ta, st);
+    if (small)
+        return a.out_f32 || a.split > 1 ? launch<MODE, 32, 1, true>(a, small_tiles, sms, dev, ta, tb, ta, st)
+                                        : launch<MODE, 32, 1, false>(a, small_tiles, sms, dev, ta, tb, ta, st);
+    const int64_t tiles = most_tiles(E, rows, 256, (a.M + 255) / 256);
+    return a.out_f32 ? launch<MODE, 256, 2, true>(a, tiles, sms, dev, ta, tb, ta, st)
+                     : launch<MODE, 256, 2, false>(a, tiles, sms, dev, ta, tb, ta, st);
 }
 
 }  // namespace
@@ -726,5 +763,9 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
         !encode_map(&to, a.out_f32 ? E_F32 : E_BF16, 3, d_dw, dims, strides, box))
         return MOE_ERR_CUDA;
     a.box = 256;   // one map of the columns
-    return launch<DW, 256, 1, false>(a, ta, tb, to, st);
+    a.split = 1;
+    int sms = 0, dev = 0;
+    if (int rc = device_sms(&sms, &dev)) return rc;
+    const int64_t tiles = (int64_t)experts * ((out + 127) / 128) * ((in + 255) / 256);
+    return launch<DW, 256, 1, false>(a, tiles, sms, dev, ta, tb, to, st);
 }

@@ -64,6 +64,7 @@ struct Args {
     int wide;          // output rows are 32-byte aligned
     int E, rows;
     int M, blocks;     // features; 128-column blocks
+    int split;         // FEW: CTAs of a cluster that share a tile's blocks
     int stages;
     int box;           // smallest height of a copy of the rows
     long long wait;    // limit of every bounded wait, in SM clock cycles
@@ -152,7 +153,10 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
-    PlanWalk tiles(tab, s_live, blocks, (a.M + NF - 1) / NF, blockIdx.x, gridDim.x);
+    const int rank = FEW ? (int)cluster_rank() : 0;
+    PlanWalk tiles(tab, s_live, blocks, (a.M + NF - 1) / NF, blockIdx.x / a.split, gridDim.x / a.split);
+    int split = a.split, blo, bhi;   // this CTA's blocks [blo, bhi)
+    tiles.split_steps(a.blocks, rank, split, blo, bhi);
     PlanTile v;
 
     if (warp < 4) {
@@ -170,9 +174,9 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                                  [&] {
                                      if (!tiles.next(v)) return -1;
                                      u = row_units(v.n, a.box);
-                                     return a.blocks;
+                                     return bhi - blo;
                                  },
-                                 [&](int b, uint32_t bar, uint32_t sa, int st) {
+                                 [&](int s, uint32_t bar, uint32_t sa, int st) {
                                      int wipe = 0;
                                      if (!FEW) {
                                          wipe = max(0, min((int)(tall >> (4 * st) & 15) + 1, CFG::NR / a.box) - u);
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                                      }
                                      const uint32_t sr = sa + WEIGHTS;
                                      mbar_expect_tx(bar, (uint32_t)((u + wipe) * a.box * 128));
-                                     tma_rows(sr, tm_rows, 128 * b, v.r0, u, a.box, bar);
+                                     tma_rows(sr, tm_rows, 128 * (blo + s), v.r0, u, a.box, bar);
                                      if (wipe) tma_rows(sr + u * a.box * 128, tm_rows, 0, a.rows, wipe, a.box, bar);
                                  });
             }
@@ -190,10 +194,10 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
             // ============ copies of the weights
             if (elect1())
                 copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
-                                 [&] { return tiles.next(v) ? a.blocks : -1; },
-                                 [&](int b, uint32_t bar, uint32_t sa, int) {
+                                 [&] { return tiles.next(v) ? bhi - blo : -1; },
+                                 [&](int s, uint32_t bar, uint32_t sa, int) {
                                      mbar_expect_tx(bar, WEIGHTS);
-                                     tma_3d(sa, &tm_w, 128 * b, v.m * NF, v.e, bar);
+                                     tma_3d(sa, &tm_w, 128 * (blo + s), v.m * NF, v.e, bar);
                                  });
             __syncwarp();
             drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                 bool ok = true;
                 while (ok && tiles.next(v)) {
                     const uint32_t id = idesc_e4m3<1>(FEW ? mma_rows<1>(v.n) : NF);
-                    for (int b = 0; b < a.blocks; b++) {
+                    for (int b = blo; b < bhi; b++) {
                         if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
                         if (!(ok = mbar_wait(smem_u32(&acc_empty[buf]), bph ^ 1, abort_v, a.wait, err))) break;
                         fence_after();
@@ -225,6 +229,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
             }
             __syncwarp();
         }
+        if (FEW && split > 1) split_others();
     } else {
         if (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // ============ sums.  MANY: rows 32 q + lane, CW features from c0 on; FEW: feature
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
         const int q = warp & 3, c0 = CW * ((warp - 4) >> 2), nb = (a.M + 127) / 128;
         int buf = 0;
         uint32_t bph = 0;
-        bool ok = true;
+        bool ok = true, reduced = false;
         while (ok && tiles.next(v)) {
             const int m0 = v.m * NF + (FEW ? 32 * q : c0);            // the warp's first feature
             const bool works = m0 < a.M && (FEW || 32 * q < v.n);     // the warp has features and rows
@@ -244,15 +249,15 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
             auto fetch = [&](int b0) {
 #pragma unroll
                 for (int g = 0; g < GROUP; g++) {
-                    const bool in = scales && b0 + g < a.blocks;
+                    const bool in = scales && b0 + g < bhi;
                     xs[g] = fetch_f32(xsp + (int64_t)(b0 + g) * a.rows, in);
                     ws[g] = fetch_f32(wsp + b0 + g, in);
                 }
             };
 #pragma unroll
             for (int c = 0; c < CW; c++) acc[c] = 0.0f;
-            fetch(0);
-            for (int b0 = 0; ok && b0 < a.blocks; b0 += GROUP) {
+            fetch(blo);
+            for (int b0 = blo; ok && b0 < bhi; b0 += GROUP) {
                 float s[GROUP];
 #pragma unroll
                 for (int g = 0; g < GROUP; g++) {
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                 fetch(b0 + GROUP);
 #pragma unroll
                 for (int g = 0; g < GROUP; g++) {
-                    if (b0 + g >= a.blocks) break;
+                    if (b0 + g >= bhi) break;
                     if (!(ok = mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort_v, a.wait, err))) break;
                     fence_after();
                     if (works) {
@@ -304,7 +309,12 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                 }
             }
             if (!ok) break;
-            if (FEW) {
+            if constexpr (FEW) {
+                if (split > 1) {
+                    split_reduce(acc, ring, rank, split, 32 * q + lane);
+                    reduced = true;
+                    if (rank) break;
+                }
                 if (m0 + lane < a.M) {
                     const int64_t at = (int64_t)v.r0 * a.ldo + m0 + lane;
                     float* of = static_cast<float*>(a.out) + at;
@@ -344,6 +354,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
             }
             __syncwarp();
         }
+        if (FEW && split > 1 && !reduced) split_others();   // no tile, or a wait that ran out
     }
     fence_before();
     __syncthreads();
@@ -354,12 +365,11 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
 }
 
 template <class CFG>
-int launch(Args& a, const RowMaps& tr, const CUtensorMap& tw, cudaStream_t st)
+int launch(Args& a, int64_t tiles, int sms, int dev, const RowMaps& tr, const CUtensorMap& tw, cudaStream_t st)
 {
     static std::atomic<int> smem_set[kMaxDevices];
     auto* kern = gg8_kernel<CFG>;
-    int sms = 0;
-    if (int rc = prepare_launch(kern, kSmemMax - kStatic, smem_set, &sms)) return rc;
+    if (int rc = allow_smem(kern, kSmemMax - kStatic, smem_set, dev)) return rc;
     const int fixed = plan_bytes(a.E);
     a.stages = (kSmemMax - kStatic - fixed) / CFG::STAGE;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
@@ -373,7 +383,7 @@ int launch(Args& a, const RowMaps& tr, const CUtensorMap& tw, cudaStream_t st)
     }
     ProfScope ps(MOE_PROF_GEMM, st);
     prof_count(MOE_PROF_GEMM, 1);
-    MOE_CUDA_TRY(launch_clusters(kern, sms, 1, CFG::THREADS, smem, st, tr, tw, a));
+    MOE_CUDA_TRY(launch_clusters(kern, sms, tiles, a.split, CFG::THREADS, smem, st, tr, tw, a));
     return MOE_OK;
 }
 
@@ -419,7 +429,12 @@ extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, co
     a.blocks = (in + 127) / 128;
     a.wait = test_wait_cycles(kWaitCycles);
     a.withhold = test_withhold();
-    const bool few = rows <= 16 * (int64_t)experts;
+    int sms = 0, dev = 0;
+    if (int rc = device_sms(&sms, &dev)) return rc;
+    // FEW where the experts have few rows, or where its small tiles fit the SMs at once
+    const int64_t few_tiles = most_tiles(experts, rows, 32, (out + 127) / 128);
+    const bool few = rows <= 16 * (int64_t)experts || few_tiles <= sms;
+    a.split = few ? split_of(few_tiles, a.blocks, sms) : 1;
     a.box = few ? 16 : 32;
     RowMaps tr;
     CUtensorMap tw;
@@ -430,5 +445,6 @@ extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, co
         !encode_map(&tw, E_U8, 3, d_wq, wd, wst, wb))
         return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return few ? launch<Cfg<true>>(a, tr, tw, st) : launch<Cfg<false>>(a, tr, tw, st);
+    return few ? launch<Cfg<true>>(a, few_tiles, sms, dev, tr, tw, st)
+               : launch<Cfg<false>>(a, most_tiles(experts, rows, 128, (out + 255) / 256), sms, dev, tr, tw, st);
 }

@@ -55,6 +55,42 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// ------------------------------------------------------------------ inner index split over a cluster
+// Calls whose tiles leave most SMs without work give each tile to a cluster of
+// a.split CTAs, a share of the inner index each (at most one tile a cluster).
+// Their sums meet in the first CTA's shared memory, where the ring was, and
+// are added there in the CTAs' order: the same bits every time.
+// Called by the warps that hold the sums, `index` the thread's place among
+// 128; every other warp of the CTA calls split_others once its work is done.
+template <int N>
+__device__ __forceinline__ void split_reduce(float (&sum)[N], unsigned char* ring, int rank, int split, int index)
+{
+    cluster_sync();   // no CTA's copies or MMAs use the rings any more
+    if (rank > 0) {
+        const uint32_t to = peer_addr(smem_u32(ring) + (uint32_t)(((rank - 1) * N * 128 + index) * 4), 0);
+#pragma unroll
+        for (int c = 0; c < N; c++) st_cluster(to + 512 * c, sum[c]);
+    }
+    cluster_sync();
+    if (rank == 0)
+        for (int r = 1; r < split; r++) {
+            const float* from = reinterpret_cast<const float*>(ring) + (r - 1) * N * 128 + index;
+#pragma unroll
+            for (int c = 0; c < N; c++) sum[c] += from[128 * c];
+        }
+}
+__device__ __forceinline__ void split_others()
+{
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+}
+
 // ------------------------------------------------------------------ mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
@@ -457,6 +493,18 @@ struct PlanWalk {
         : tab(t), B(b), live(live_), mt(mt_), i(0), parts(parts_), u(part), total((long long)t[live_].pre * mt_)
     {
     }
+    // This CTA's share [lo, hi) of `steps` steps of the inner index, with the index split over
+    // a cluster.  Offsets that no call of moe_permute writes (ranges that overlap) can make
+    // more tiles than clusters: the first CTA of each then does them alone.
+    __device__ __forceinline__ void split_steps(int steps, int rank, int& split, int& lo, int& hi)
+    {
+        if (split > 1 && total > parts) {
+            if (rank) total = 0;
+            split = 1;
+        }
+        lo = split > 1 ? steps * rank / split : 0;
+        hi = split > 1 ? steps * (rank + 1) / split : steps;
+    }
     __device__ __forceinline__ bool next(PlanTile& v)
     {
         if (u >= total) return false;
@@ -492,17 +540,33 @@ __device__ __forceinline__ int mma_rows(int n)
     return (n + 16 * CG - 1) / (16 * CG) * (16 * CG);
 }
 
-// One CTA, or one cluster of CG, per SM or CG of them.
+// Most tiles that `rows` rows of E experts can make: blocks of `size` rows by mt feature tiles.
+static inline int64_t most_tiles(int E, int rows, int size, int64_t mt)
+{
+    const int64_t live = E < rows ? E : rows, blocks = rows / size + live;
+    return mt * (blocks < rows ? blocks : rows);
+}
+// CTAs to split the inner index over, given the most tiles (of few rows) and
+// the steps of a tile: as many as leave every tile its cluster on three
+// quarters of the SMs (clusters do not pack them all) and four steps a CTA.
+static inline int split_of(int64_t tiles, int steps, int sms)
+{
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms * 3 / 4 && steps >= 8 * split) split *= 2;
+    return split;
+}
+
+// CTAs in clusters of CG: one CTA an SM, but no more clusters than tiles.
 template <class... P, class... A>
-static inline cudaError_t launch_clusters(void (*kern)(P...), int sms, int CG, int threads, int smem, cudaStream_t st,
-                                          const A&... args)
+static inline cudaError_t launch_clusters(void (*kern)(P...), int sms, int64_t tiles, int CG, int threads, int smem,
+                                          cudaStream_t st, const A&... args)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = CG;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms / CG * CG);
+    cfg.gridDim = dim3((unsigned)(tiles < sms / CG ? tiles : sms / CG) * CG);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -529,23 +593,25 @@ static inline bool rows_ok(const void* p, int64_t ld, int64_t width, int size)
 static inline bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_BF16; }
 static inline int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
 
-// SMs of the current device.  The first launch of a kernel on a device also
-// lets it use `most` bytes of dynamic shared memory (`smem_set`: one flag a
-// device).
-template <class K>
-static inline int prepare_launch(K* kern, int most, std::atomic<int>* smem_set, int* sms)
+// SMs of the current device, and its number.
+static inline int device_sms(int* sms, int* dev)
 {
     static std::atomic<int> count[kMaxDevices];
-    int dev = 0;
-    MOE_CUDA_TRY(cudaGetDevice(&dev));
-    if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
-    if (!(*sms = count[dev].load(std::memory_order_relaxed))) {
-        MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
-        count[dev].store(*sms, std::memory_order_relaxed);
+    MOE_CUDA_TRY(cudaGetDevice(dev));
+    if (*dev < 0 || *dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+    if (!(*sms = count[*dev].load(std::memory_order_relaxed))) {
+        MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev));
+        count[*dev].store(*sms, std::memory_order_relaxed);
     }
-    if (!smem_set[dev].load(std::memory_order_relaxed)) {
+    return MOE_OK;
+}
+// Lets a kernel use `most` bytes of dynamic shared memory, once a device (`set`: a flag each).
+template <class K>
+static inline int allow_smem(K* kern, int most, std::atomic<int>* set, int dev)
+{
+    if (!set[dev].load(std::memory_order_relaxed)) {
         MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-        smem_set[dev].store(1, std::memory_order_relaxed);
+        set[dev].store(1, std::memory_order_relaxed);
     }
     return MOE_OK;
 }

@@ -274,11 +274,12 @@ def _dims(t, n):
 
 
 def _ld(strides, rows, cols) -> int:
-    """Leading dimension of a row matrix whose columns are adjacent, 0 of any other."""
+    """Leading dimension of a row matrix whose columns are adjacent, 0 of any other (one row has no
+    next: its stride does not count)."""
     a, b = strides
     if b != 1:
         return 0
-    return a if a >= cols else cols if rows <= 1 else 0
+    return cols if rows <= 1 else a if a >= cols else 0
 
 
 def _device() -> int:

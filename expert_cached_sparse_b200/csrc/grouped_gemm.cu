@@ -26,10 +26,11 @@
 // features instead of once for 128.
 //
 // Roles, one persistent CTA or pair per SM or two: warps 0 and 2 copy the two
-// operands, warp 1 (of the pair's first CTA) issues the MMAs into one of two
-// accumulators, warps 4-7 read the other one back and store it.  Warp 3 works
-// between copies and MMAs where that is needed: it zeroes the surplus rows
-// (DW) and tells the pair's first CTA that a stage is in place (CG = 2).
+// operands (one warp for both issued too slowly), warp 1 (of the pair's first
+// CTA) issues the MMAs into one of two accumulators, warps 4 on read the other
+// one back and store it.  Warp 3 works between copies and MMAs where that is
+// needed: it zeroes the surplus rows (DW) and tells the pair's first CTA that a
+// stage is in place (CG = 2).
 // Every wait is bounded; a timeout records MOE_ERR_TIMEOUT, raises the CTA's
 // abort flag so that the other roles stop, and the CTA waits for its own
 // copies and MMAs before it returns.
@@ -95,7 +96,6 @@ struct Units {
     const Args& a;
     PlanWalk walk;
     const int rank;
-
     int split, s0, s1;   // CG = 1: the cluster's CTAs that share the inner index, this one's steps
 
     __device__ Units(const Args& a_, const PlanExpert* tab, const int*, int live, int rank_)
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                             const uint64_t db = MODE == DW ? desc_mn(sb, 8192) : desc_k(sb);
                             // 16 inner indices: 32 bytes along a K-major row, 16 rows MN-major
                             const int kk = MODE == DW && s == v.steps - 1 ? (v.tail + 15) / 16 : 4;
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 4; k++)
                                 if (MODE != DW || k < kk)
                                     mma_bf16<CG>(d, da + k * (MODE == FWD ? 2 : 128), db + k * (MODE == DW ? 128 : 2), id,
@@ -442,7 +442,6 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                                 for (int c = 0; c < chunks; c++)
                                     *reinterpret_cast<uint4*>(p + 8192 * c + i) = make_uint4(0, 0, 0, 0);
                             asm volatile("fence.proxy.async;" ::: "memory");
-                            if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                             __syncwarp();
                         }
                         if (lane == 0) {

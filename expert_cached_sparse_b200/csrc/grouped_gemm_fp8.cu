@@ -50,7 +50,8 @@ struct Cfg {
 // latter hold 128 sums each: together what the block is launched with,
 // 128 * 72 + 256 * 216 = 384 * 168.
 constexpr int kRegs = 168, kControlRegs = 72, kSumRegs = 216;
-static_assert(128 * kControlRegs + 32 * Cfg<false>::EPI * kSumRegs <= Cfg<false>::THREADS * kRegs, "a larger split never starts");
+static_assert(128 * kControlRegs + 32 * Cfg<false>::EPI * kSumRegs <= Cfg<false>::THREADS * kRegs,
+              "a larger split never starts");
 constexpr int kMaxStages = 12;
 constexpr int kStatic = 4096;        // bytes of static shared memory at most
 
@@ -208,14 +209,14 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                 uint32_t ph = 0, bph = 0;
                 bool ok = true;
                 while (ok && tiles.next(v)) {
-                    const uint32_t id = idesc_e4m3<1>(FEW ? mma_rows<1>(v.n) : NF);
+                    const uint32_t id = idesc_e4m3(FEW ? mma_rows<1>(v.n) : NF);
                     for (int b = blo; b < bhi; b++) {
                         if (!(ok = mbar_wait(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
                         if (!(ok = mbar_wait(smem_u32(&acc_empty[buf]), bph ^ 1, abort_v, a.wait, err))) break;
                         fence_after();
                         const uint32_t sa = smem_u32(ring + (size_t)st * STAGE);
                         const uint64_t da = desc_k(FEW ? sa : sa + WEIGHTS), db = desc_k(FEW ? sa + WEIGHTS : sa);
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < 4; k++)
                             mma_e4m3<1>(tmem + (uint32_t)(buf * CFG::COLS), da + 2 * k, db + 2 * k, id, k > 0);
                         commit<1>(smem_u32(&empty[st]));

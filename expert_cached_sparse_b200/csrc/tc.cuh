@@ -26,7 +26,7 @@ __device__ __forceinline__ bool elect1()
     return e != 0;
 }
 
-// ------------------------------------------------------------------ clusters (CTA pairs)
+// ------------------------------------------------------------------ clusters
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -296,20 +296,16 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t chunk)
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// Instruction descriptor, fp32 accumulators, M = 128 CG, N = n (a multiple of
-// 16 CG): bf16 operands (kind::f16) with either operand MN-major, or e4m3
-// (kind::f8f6f4, K-major, every format field 0).
+// Instruction descriptor, fp32 accumulators, M = 128 (128 CG), N = n (a
+// multiple of 16 CG): bf16 operands (kind::f16) with either operand MN-major,
+// or e4m3 (kind::f8f6f4, K-major, every format field 0).
 template <int CG>
 __device__ __forceinline__ uint32_t idesc_bf16(int n, bool a_mn, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(n >> 3) << 17) | (8u * CG << 24);
 }
-template <int CG>
-__device__ __forceinline__ uint32_t idesc_e4m3(int n)
-{
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u * CG << 24);
-}
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
 
 // D[tmem] (+)= A[smem] B[smem], K = 16 bf16 or 32 e4m3 columns.  A pair's MMA
 // is issued by its first CTA: each CTA holds 128 rows of A, half of B's N rows
@@ -396,12 +392,13 @@ bool encode_rows(RowMaps* r, Elem type, const void* p, int64_t ld, int width, in
 
 // ------------------------------------------------------------------ the plan of a call
 // A call's tiles run through its experts, an expert's feature tiles, and
-// fastest the blocks of rows of a feature tile.  CTA (or pair) c takes tiles c, c + G, c + 2 G, ... of G,
-// so that what runs at one time is neighbours, which share weights and rows in
-// L2 (equal contiguous runs of tiles, one a CTA, took 1.4 to 1.8 times as
-// long on 4096 tokens: each expert's rows were read again for every feature
-// tile; the largest experts first, for even rounds, took up to 1.25 times as
-// long: tiles bound by their weights no longer ran beside those bound by MMAs).
+// fastest the blocks of rows of a feature tile.  CTA (or cluster) c of G takes
+// tiles c, c + G, c + 2 G, ..., so that what runs at one time is neighbours,
+// which share weights and rows in L2.  (Equal contiguous runs of tiles, one a
+// CTA, took 1.4 to 1.8 times as long on 4096 tokens: each expert's rows were
+// read again for every feature tile.  The largest experts first, for even
+// rounds, took up to 1.25 times as long: tiles bound by their weights no longer
+// ran beside those bound by MMAs.)
 struct PlanExpert {
     int pre;       // blocks of the experts before
     int e, r0, r1; // expert and its rows

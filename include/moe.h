@@ -523,9 +523,11 @@ int moe_act_terms(const void* d_x, int32_t x_dtype, int32_t rows, int32_t K, int
  *    leading dimensions of 16-bit and 8-bit ones 16-byte aligned; no output
  *    may overlap an input;
  *  - products are summed in fp32 and rounded once to the output type
- *    (float32 or bf16, nearest even).  The same inputs give the same bits on
- *    every call.  No workspace, nothing read back: every call can be captured
- *    in a CUDA graph, and calls on different streams may overlap.
+ *    (float32 or bf16, nearest even); the tensor core truncates as it adds, so
+ *    float32 results are off by up to about 5e-7 relative (2-norm).  The same
+ *    inputs give the same bits on every call.  No workspace, nothing read
+ *    back: every call can be captured in a CUDA graph, and calls on different
+ *    streams may overlap.
  * Errors: MOE_ERR_INVALID_ARG for bad sizes, types, alignments or NULL
  * pointers, MOE_ERR_UNSUPPORTED for sizes above the limits.
  * Pages: experts found in VRAM execute on the GPU ("FreeToken quantization",
@@ -556,8 +558,9 @@ int moe_grouped_gemm_dx(int32_t experts, int32_t in, int32_t out, const uint16_t
  * the rows r of e of dy[r] x[r]^T.  d_dy [rows][out] bf16 (lddy), d_x
  * [rows][in] bf16 (ldx), d_dw [experts][out][in] in dw_dtype.  accumulate ==
  * 0 stores the sum (zeros for an expert without rows); otherwise it is added
- * to what d_dw holds (in fp32, then rounded to dw_dtype), and an expert
- * without rows is left as it was.  rows may be 0.
+ * to what d_dw holds (in fp32, then rounded to dw_dtype; float32 sums below
+ * 2^-126 may become 0), and an expert without rows is left as it was.  rows
+ * may be 0.
  */
 int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, const uint16_t* d_dy, int64_t lddy,
                         const uint16_t* d_x, int64_t ldx, const int32_t* d_offsets, int32_t rows, void* d_dw,
@@ -583,8 +586,8 @@ int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, const uint8_t
  * Rows -> e4m3 codes with one float32 scale per 128 columns of a row (the
  * last block may be shorter).  With swiglu == 0 the row is d_x [rows][cols]
  * (x_dtype, ldx); otherwise d_x is [rows][2 cols], gate then up, and the row
- * is silu(gate) * up in fp32 (relative error below (10 + 1.5 |gate|) 2^-24),
- * not rounded in between.  For a block of
+ * is silu(gate) * up in fp32 (relative error below (10 + 1.5 |gate|) 2^-24;
+ * gates below -87 may give 0), not rounded in between.  For a block of
  * largest magnitude m (NaN left out): s = m / 448, or 1 when m < 2^-100;
  * q = the e4m3 code nearest to x / s (ties to even), division and quotient in
  * fp32; codes of a block below 2^-100 are zeros.  A NaN becomes a NaN code;

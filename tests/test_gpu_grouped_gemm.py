@@ -7,6 +7,10 @@ the sums, and float32 outputs must equal the 64-bit reference bit for bit;
 bf16 outputs must equal its rounding.  Normal inputs are held to bounds
 derived where they are used.
 """
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -155,6 +159,41 @@ def test_long_inner_sizes(K):
         a = fp8_inputs(E, rows, K, N, g)
         A.moe_grouped_gemm_fp8(*a, off, y)
         assert torch.equal(y.double(), ref_fp8(*a, off))
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+def test_many_rows_over_long_inner_sizes(dt):
+    """Tiles of many rows (pairs of CTAs) whose inner sizes take several partial sums and several rounds
+    of the stages, off every tile edge."""
+    counts, K, N = [600, 0, 257, 3], 1552, 1160
+    g, rows, E = gen(15), sum(counts), len(counts)
+    off = offsets_of(counts)
+    x, w, dy = ints((rows, K), g), ints((E, N, K), g), ints((rows, N), g)
+    y, dx = torch.empty(rows, N, dtype=dt, device=DEV), torch.empty(rows, K, dtype=dt, device=DEV)
+    A.moe_grouped_gemm(x, w, off, y)
+    assert torch.equal(y, ref_fwd(x, w, off).to(dt))
+    A.moe_grouped_gemm_dx(dy, w, off, dx)
+    assert torch.equal(dx, ref_dx(dy, w, off).to(dt))
+    a = fp8_inputs(E, rows, K, N, g)
+    A.moe_grouped_gemm_fp8(*a, off, y)
+    assert torch.equal(y, ref_fp8(*a, off).to(dt))
+
+
+def test_overlapping_ranges_end():
+    """Ranges that share rows make more tiles than a call of these sizes can need.  What the shared rows
+    get is one of the experts' products (here the same for all), and the call ends."""
+    rows, E, K, N = 4, 9, 2048, 128
+    g = gen(16)
+    off = torch.tensor([0, 4] * 5, dtype=torch.int32, device=DEV)[: E + 1]     # (0,4) (4,0) (0,4) ...
+    x, w = ints((rows, K), g), ints((1, N, K), g).expand(E, N, K).contiguous()
+    y = torch.empty(rows, N, dtype=F32, device=DEV)
+    A.moe_grouped_gemm(x, w, off, y)
+    assert torch.equal(y.double(), x.double() @ w[0].double().t())
+    a = list(fp8_inputs(1, rows, K, N, g))
+    a[2], a[3] = a[2].expand(E, N, K).contiguous(), a[3].expand(E, 1, 16).contiguous()
+    A.moe_grouped_gemm_fp8(*a, off, y)
+    assert torch.equal(y.double(), ref_fp8(a[0], a[1], a[2][:1], a[3][:1], offsets_of([rows])))
+    assert A.moe_get_device_error() == 0
 
 
 def _norm_bound(K, S, ref, dt):
@@ -322,6 +361,14 @@ def test_column_slices_of_wider_matrices():
     assert bool((yw[:, :8] == 7).all() and (yw[:, 8 + N:] == 7).all())
 
 
+def test_one_rows_stride_does_not_count():
+    g = gen(18)
+    x, w = ints((3, 75), g)[:1, :72], ints((1, 136, 72), g)
+    y = torch.zeros(3, 139, dtype=F32, device=DEV)
+    A.moe_grouped_gemm(x, w, offsets_of([1]), y[:1, :136])
+    assert torch.equal(y[:1, :136].double(), ref_fwd(x, w, offsets_of([1]))) and not bool(y[1:].any() or y[:, 136:].any())
+
+
 def test_misaligned_slices_are_refused():
     x, w, y = (torch.zeros(s, dtype=BF, device=DEV) for s in ((8, 72), (1, 64, 64), (8, 64)))
     off = offsets_of([8])
@@ -401,6 +448,73 @@ def test_captured_call_follows_new_offsets_and_data():
         assert torch.equal(dw.double(), ref_dw(dy, x, off))
         assert torch.equal(y8[:n].double(), ref_fp8(*f, off)[:n])
         assert torch.equal(q.to(F32), _codes(xf)[0].to(F32))
+
+
+def test_first_call_of_a_process_may_be_a_captured_one():
+    """Nothing a first call sets up (limits, symbols) is refused while a stream is being captured."""
+    code = """
+import torch
+from expert_cached_sparse_b200 import api as A
+d, bf, f8 = "cuda", torch.bfloat16, torch.float8_e4m3fn
+for counts in ([1, 2], [300, 20]):
+    rows, K, N = sum(counts), 128, 256
+    off = torch.tensor([0, counts[0], rows], dtype=torch.int32, device=d)
+    x, w, dy = (torch.ones(s, device=d).to(bf) for s in ((rows, K), (2, N, K), (rows, N)))
+    q, wq = (torch.empty(s, dtype=f8, device=d) for s in ((rows, K), (2, N, K)))
+    s, ws = torch.empty(1, rows, device=d), torch.empty(2, 2, 1, device=d)
+    outs = []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for t in (torch.float32, bf):
+            y, y8, dx, dw = (torch.empty(s, dtype=t, device=d) for s in ((rows, N), (rows, N), (rows, K), (2, N, K)))
+            A.moe_grouped_gemm(x, w, off, y)
+            A.moe_grouped_gemm_dx(dy, w, off, dx)
+            A.moe_grouped_gemm_dw(dy, x, off, dw)
+            A.moe_fp8_quantize_act(x, q, s)
+            A.moe_fp8_quantize_weight(w, wq, ws)
+            A.moe_grouped_gemm_fp8(q, s, wq, ws, off, y8)
+            outs += [(y, K), (dx, N), (y8, K), (dw[0], counts[0]), (dw[1], counts[1])]
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, (o, v) in enumerate(outs):
+        want = torch.full((), v, device=d).to(o.dtype).float()
+        assert bool(((o.float() - want).abs() <= 1e-6 * v).all()), (i, v, o.flatten()[:4])
+print("done")
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=pathlib.Path(__file__).resolve().parents[1])
+    assert out.returncode == 0 and "done" in out.stdout, out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("rows", [500, 70000])
+def test_as_many_experts_as_allowed(rows):
+    """4096 experts: the tables take most of what the stages leave."""
+    E, K, N = 4096, 80, 136
+    g = gen(17)
+    cut = torch.sort(torch.randint(0, rows + 1, (E - 1,), generator=g, device=DEV))[0]
+    off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), rows)]).to(torch.int32)
+    x, w, dy = ints((rows, K), g, 1), ints((E, N, K), g, 1), ints((rows, N), g, 1)
+    own = torch.repeat_interleave(torch.arange(E, device=DEV), off.diff().long())
+    step = 5000
+
+    def rowwise(a, m):   # rows with their own matrix
+        return torch.cat([torch.einsum("rk,rnk->rn", a[i:i + step].to(F32), m[own[i:i + step]].to(F32))
+                                        for i in range(0, rows, step)])
+
+    y, dx = torch.empty(rows, N, dtype=F32, device=DEV), torch.empty(rows, K, dtype=F32, device=DEV)
+    A.moe_grouped_gemm(x, w, off, y)
+    assert torch.equal(y, rowwise(x, w))
+    A.moe_grouped_gemm_dx(dy, w, off, dx)
+    assert torch.equal(dx, rowwise(dy, w.transpose(1, 2)))
+    dw, want = (torch.zeros(E, N, K, dtype=F32, device=DEV) for _ in range(2))
+    A.moe_grouped_gemm_dw(dy, x, off, dw)
+    for i in range(0, rows, step):
+        want.index_add_(0, own[i:i + step], dy[i:i + step].to(F32)[:, :, None] * x[i:i + step].to(F32)[:, None, :])
+    assert torch.equal(dw, want)
+    a = fp8_inputs(E, rows, K, N, g)
+    A.moe_grouped_gemm_fp8(*a, off, y)
+    want = rowwise(a[0].to(F32), a[2].to(F32)) * a[1][0][:, None] * a[3][own, :, 0].repeat_interleave(128, 1)[:, :N]
+    assert torch.equal(y, want)
 
 
 def test_offsets_past_32_bits():

@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 namespace {
@@ -118,6 +119,8 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__
     constexpr int SZ = XF32 ? 4 : 2;
     const int kb = (cols + 127) / 128, per = (kb + BPT - 1) / BPT, sub = threadIdx.x & 15;
     const int total = (rows + 15) / 16 * per;
+    start_next();
+    wait_before();
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
         const int r = i / per * 16 + (threadIdx.x >> 4), b0 = i % per * BPT;
         const char* p = static_cast<const char*>(x) + (int64_t)r * ldx * SZ;
@@ -167,6 +170,8 @@ __global__ void __launch_bounds__(256, XF32 ? 2 : 4)
     const int nb = (out + 127) / 128, kb = (in + 127) / 128;
     const int tr = threadIdx.x >> 4, c8 = (threadIdx.x & 15) * 8;
     int flip = 0;
+    start_next();
+    wait_before();
     for (int i = blockIdx.x; i < blocks; i += gridDim.x, flip ^= 1) {
         const int en = i / kb, b = i - en * kb;
         const int64_t e = en / nb;
@@ -246,8 +251,7 @@ extern "C" int moe_fp8_quantize_act(const void* d_x, int32_t x_dtype, int64_t ld
                              : (swiglu ? quant_act_kernel<false, true, 4> : quant_act_kernel<false, false, 4>))
                       : (f32 ? (swiglu ? quant_act_kernel<true, true, 1> : quant_act_kernel<true, false, 1>)
                              : (swiglu ? quant_act_kernel<false, true, 1> : quant_act_kernel<false, false, 1>));
-    kern<<<grid, 256, 0, st>>>(d_x, ldx, rows, cols, d_q, ldq, d_s);
-    MOE_LAUNCH_CHECK();
+    MOE_CUDA_TRY(launch_overlapped(kern, grid, 1, 256, 0, st, d_x, ldx, (int)rows, (int)cols, d_q, ldq, d_s));
     return MOE_OK;
 }
 
@@ -267,7 +271,6 @@ extern "C" int moe_fp8_quantize_weight(const void* d_w, int32_t w_dtype, int32_t
     const int cap = sm_count() * (w_dtype == MOE_DT_F32 ? 2 : 4);
     const int grid = (int)(blocks < cap ? blocks : cap);
     auto* kern = w_dtype == MOE_DT_F32 ? quant_weight_kernel<true> : quant_weight_kernel<false>;
-    kern<<<grid, 256, 0, st>>>(d_w, (int)blocks, out, in, d_q, d_s);
-    MOE_LAUNCH_CHECK();
+    MOE_CUDA_TRY(launch_overlapped(kern, grid, 1, 256, 0, st, d_w, (int)blocks, (int)out, (int)in, d_q, d_s));
     return MOE_OK;
 }

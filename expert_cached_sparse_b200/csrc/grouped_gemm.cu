@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
     int* err = &g_gemm_error;
 
     if (smem_u32(ring) & 1023) {   // the swizzle counts on it; static shared memory is padded so
+        wait_before();
         if (tid == 0) atomicCAS(err, 0, (int)MOE_ERR_UNSUPPORTED);
         return;
     }
@@ -307,10 +308,12 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
     }
     if (warp == 0) {
         tma_prefetch(&tm_a);
-    } else if (warp == 1) {
-        tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);
     } else if (warp == 2) {
         for (int i = 0; i < kRowMaps && a.box << i <= NB / CG; i++) tma_prefetch(&tm_b.m[i]);
+    }
+    wait_before();
+    if (warp == 1) {
+        tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);   // (not before: it may wait for what the kernel before holds)
     } else if (warp >= 4) {
         if constexpr (MODE == DW)
             for (int i = tid - 128; i <= a.E; i += 128) off[i] = __ldg(a.offsets + i);
@@ -347,6 +350,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                                          }
                                  });
             __syncwarp();
+            start_next();   // (at the kernel's start: the same within 1%, and SMs held for longer)
             drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 2) {
             // ============ copies of the columns (B)

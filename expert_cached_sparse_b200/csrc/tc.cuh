@@ -10,6 +10,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 namespace tc {
@@ -558,18 +559,7 @@ template <class... P, class... A>
 static inline cudaError_t launch_clusters(void (*kern)(P...), int sms, int64_t tiles, int CG, int threads, int smem,
                                           cudaStream_t st, const A&... args)
 {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles < sms / CG ? tiles : sms / CG) * CG);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    return launch_overlapped(kern, (int)(tiles < sms / CG ? tiles : sms / CG) * CG, CG, threads, smem, st, args...);
 }
 
 // ------------------------------------------------------------------ host: checks common to the products

@@ -450,6 +450,58 @@ def test_captured_call_follows_new_offsets_and_data():
         assert torch.equal(q.to(F32), _codes(xf)[0].to(F32))
 
 
+def test_calls_back_to_back_wait_for_each_other():
+    """Kernels may start while the one before them ends: every call of a chain still reads what the calls
+    before it wrote, and writes what they no longer read, on a stream and in a graph."""
+    E, K, N, rows = 5, 256, 384, 90
+    g = gen(19)
+    off = offsets_of([20, 0, 33, 1, 36])
+    w1, w2 = (ints((E, a, b), g, 1) for a, b in ((N, K), (K, N)))
+    q1, q2 = torch.empty(E, N, K, dtype=F8, device=DEV), torch.empty(E, N, K, dtype=F8, device=DEV)
+    s1 = torch.empty(E, N // 128, K // 128, device=DEV)
+    s2 = torch.empty_like(s1)
+    x0 = torch.randn(rows, K, generator=g, device=DEV).to(BF)
+    x, y = torch.empty_like(x0), torch.empty(rows, N, dtype=BF, device=DEV)
+    q, s = torch.empty(rows, K, dtype=F8, device=DEV), torch.empty(K // 128, rows, device=DEV)
+    y8, dw = torch.empty(rows, N, device=DEV), torch.empty(E, N, K, device=DEV)
+    ids = torch.zeros(rows, K, device=DEV)
+
+    def chain(pause):
+        st = torch.cuda.current_stream()
+        x.copy_(x0)
+        for i in range(12):
+            for f in (lambda: A.moe_grouped_gemm(x, w1, off, y, stream=st),
+                      lambda: A.moe_grouped_gemm(y, w2, off, x, stream=st),
+                      lambda: x.mul_(1 / 256),
+                      lambda: A.moe_grouped_gemm_dw(y, x, off, dw, accumulate=i > 0, stream=st),
+                      lambda: A.moe_fp8_quantize_act(x, q, s, stream=st),
+                      lambda: A.moe_fp8_quantize_weight(dw, q1 if i % 2 else q2, s1 if i % 2 else s2, stream=st),
+                      lambda: A.moe_grouped_gemm_fp8(q, s, q1 if i % 2 else q2, s1 if i % 2 else s2, off, y8, stream=st),
+                      lambda: ids.add_(y8[:, :K])):
+                f()
+                if pause:
+                    torch.cuda.synchronize()
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (x, y, dw, y8, ids, s, s1, s2, q.to(F32), q1.to(F32), q2.to(F32))]
+
+    chain(True)
+    want = results()
+    assert all(bool(torch.isfinite(t).all()) for t in want) and bool(want[3].any())
+    ids.zero_()
+    chain(False)
+    assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    ids.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(False)
+    for _ in range(3):
+        ids.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+
+
 def test_first_call_of_a_process_may_be_a_captured_one():
     """Nothing a first call sets up (limits, symbols) is refused while a stream is being captured."""
     code = """
@@ -465,15 +517,18 @@ for counts in ([1, 2], [300, 20]):
     outs = []
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
+        st = torch.cuda.current_stream()
         for t in (torch.float32, bf):
             y, y8, dx, dw = (torch.empty(s, dtype=t, device=d) for s in ((rows, N), (rows, N), (rows, K), (2, N, K)))
-            A.moe_grouped_gemm(x, w, off, y)
-            A.moe_grouped_gemm_dx(dy, w, off, dx)
-            A.moe_grouped_gemm_dw(dy, x, off, dw)
-            A.moe_fp8_quantize_act(x, q, s)
-            A.moe_fp8_quantize_weight(w, wq, ws)
-            A.moe_grouped_gemm_fp8(q, s, wq, ws, off, y8)
+            A.moe_grouped_gemm(x, w, off, y, stream=st)
+            A.moe_grouped_gemm_dx(dy, w, off, dx, stream=st)
+            A.moe_grouped_gemm_dw(dy, x, off, dw, stream=st)
+            A.moe_fp8_quantize_act(x, q, s, stream=st)
+            A.moe_fp8_quantize_weight(w, wq, ws, stream=st)
+            A.moe_grouped_gemm_fp8(q, s, wq, ws, off, y8, stream=st)
             outs += [(y, K), (dx, N), (y8, K), (dw[0], counts[0]), (dw[1], counts[1])]
+    for o, _ in outs:
+        o.fill_(7)
     graph.replay()
     torch.cuda.synchronize()
     for i, (o, v) in enumerate(outs):

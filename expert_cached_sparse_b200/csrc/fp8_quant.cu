@@ -14,7 +14,57 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyBlock = 7.888609052210118e-31f;   // 2^-100
 constexpr int64_t kMaxDim = 1 << 20;
 
-__device__ __forceinline__ float block_scale(float m) { return m < kTinyBlock ? 1.0f : __fdiv_rn(m, kE4m3Max); }
+// Two floats at a time: one instruction for both, each rounded by itself.
+struct Two {
+    unsigned long long v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b)
+{
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
+// Quotients by Markstein's method (P. W. Markstein, IBM J. Res. Dev. 34, 1990):
+// with y the correctly rounded 1 / s, q0 = v y and the exact residual
+// r = v - q0 s, q0 + r y rounds to the correctly rounded v / s: three
+// instructions an element against about forty of a division.
+__device__ __forceinline__ float quotient(float v, float s, float y)
+{
+    const float q = __fmul_rn(v, y);
+    return __fmaf_rn(__fmaf_rn(-q, s, v), y, q);
+}
+__device__ __forceinline__ float block_scale(float m)
+{
+    if (isinf(m)) return m;
+    return m < kTinyBlock ? 1.0f : quotient(m, kE4m3Max, 1.0f / kE4m3Max);
+}
+// 1 / s, correctly rounded, for 2^-109 <= s < 2^120: two Newton steps from the
+// hardware's reciprocal; the second one rounds correctly unless the
+// significand of s is all ones (the same paper).
+__device__ __forceinline__ float reciprocal(float s)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    y = __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
+    y = __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
+    return (__float_as_uint(s) & 0x7FFFFF) == 0x7FFFFF ? __fdiv_rn(1.0f, s) : y;
+}
 
 // Eight consecutive elements as they lie in memory; bf16 ones stay packed
 // (four registers instead of eight while loads are in flight).
@@ -67,34 +117,36 @@ __device__ __forceinline__ float max8(const float (&v)[8])
 // silu(g) * u with the hardware's 2^x (relative error 2^-22) and reciprocal
 // (2^-23): with the roundings of -g log2(e), of the sum and of the products
 // the relative error is below (10 + 1.5 |g|) 2^-24, far inside an e4m3 step of
-// 2^-4.  Six instructions an element; expf and a division took 32 in all, and
-// this kernel is bound by its instructions (44% of HBM, 79% of issue slots).
-__device__ __forceinline__ float swiglu1(float g, float u)
+// 2^-4.  Four instructions an element; expf and a division took 32 in all, and
+// this kernel is bound by its instructions.
+__device__ __forceinline__ Two swiglu2(Two g, Two u)
 {
-    float t, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-    return g * r * u;
+    float a, b;
+    mul2(g, Two(-1.4426950408889634f, -1.4426950408889634f)).get(a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    add2(Two(a, b), Two(1.0f, 1.0f)).get(a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return mul2(mul2(g, Two(a, b)), u);
 }
 
-// The block's divisor: v / s for its 128 or 16384 elements by Markstein's
-// method (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with y the correctly
-// rounded 1 / s, q0 = v y and the exact residual r = v - q0 s, q0 + r y rounds
-// to the correctly rounded v / s: three instructions an element against about
-// forty of a division.  An infinite s gives y = 0 and takes the part of a zero
-// in the residual, so that finite / inf is 0 and inf / inf NaN.  Quotients
-// whose residual underflows are below 2^-16: code 0 either way.
+// The block's divisor: v / s for its 128 or 16384 elements.  An infinite s
+// gives y = 0 and takes the part of a zero in the residual, so that
+// finite / inf is 0 and inf / inf NaN.  Quotients whose residual underflows are
+// below 2^-16: code 0 either way.
 struct Divisor {
-    float s, y;
+    Two s, y;   // -s twice, 1 / s twice
     __device__ __forceinline__ explicit Divisor(float scale)
     {
-        s = isinf(scale) ? 0.0f : scale;
-        y = isinf(scale) ? 0.0f : __fdiv_rn(1.0f, scale);
+        const float t = isinf(scale) ? 0.0f : scale, r = isinf(scale) ? 0.0f : reciprocal(scale);
+        s = Two(-t, -t);
+        y = Two(r, r);
     }
-    __device__ __forceinline__ float operator()(float v) const
+    __device__ __forceinline__ Two operator()(Two v) const
     {
-        const float q = __fmul_rn(v, y);
-        return __fmaf_rn(__fmaf_rn(-q, s, v), y, q);
+        const Two q = mul2(v, y);
+        return fma2(fma2(q, s, v), y, q);
     }
 };
 
@@ -103,7 +155,8 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Divisor& d)
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float2 r = make_float2(d(v[2 * i]), d(v[2 * i + 1]));
+        float2 r;
+        d(Two(v[2 * i], v[2 * i + 1])).get(r.x, r.y);
         w[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
     }
     return make_uint2(w[0], w[1]);
@@ -145,7 +198,7 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__
                 float u[8];
                 u8[j].get(u);
 #pragma unroll
-                for (int k = 0; k < 8; k++) v[k] = swiglu1(v[k], u[k]);
+                for (int k = 0; k < 8; k += 2) swiglu2(Two(v[k], v[k + 1]), Two(u[k], u[k + 1])).get(v[k], v[k + 1]);
             }
             float m = max8(v);
 #pragma unroll

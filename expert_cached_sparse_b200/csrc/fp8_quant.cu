@@ -54,7 +54,7 @@ __device__ __forceinline__ float block_scale(float m)
     if (isinf(m)) return m;
     return m < kTinyBlock ? 1.0f : quotient(m, kE4m3Max, 1.0f / kE4m3Max);
 }
-// 1 / s, correctly rounded, for 2^-109 <= s < 2^120: two Newton steps from the
+// 1 / s, correctly rounded, for 2^-90 <= s < 2^120: two Newton steps from the
 // hardware's reciprocal; the second one rounds correctly unless the
 // significand of s is all ones (the same paper).
 __device__ __forceinline__ float reciprocal(float s)
@@ -133,12 +133,19 @@ __device__ __forceinline__ Two swiglu2(Two g, Two u)
 
 // The block's divisor: v / s for its 128 or 16384 elements.  An infinite s
 // gives y = 0 and takes the part of a zero in the residual, so that
-// finite / inf is 0 and inf / inf NaN.  Quotients whose residual underflows are
-// below 2^-16: code 0 either way.
+// finite / inf is 0 and inf / inf NaN.  The residual's last bit is worth
+// 2^-46 times the leading ones of s and of the quotient: no less than 2^-149,
+// so exact, where s >= 2^-92 and the quotient is at least 2^-11 (codes of
+// smaller ones are 0 either way).  Smaller s, and their v, are scaled up.
+constexpr float kLift = 1.8446744073709552e19f;        // 2^64
+constexpr float kSmallScale = 8.077935669463161e-28f;   // 2^-90
 struct Divisor {
-    Two s, y;   // -s twice, 1 / s twice
+    Two s, y;    // -s twice, 1 / s twice
+    bool lift;
     __device__ __forceinline__ explicit Divisor(float scale)
     {
+        lift = scale < kSmallScale;
+        if (lift) scale *= kLift;
         const float t = isinf(scale) ? 0.0f : scale, r = isinf(scale) ? 0.0f : reciprocal(scale);
         s = Two(-t, -t);
         y = Two(r, r);
@@ -150,16 +157,25 @@ struct Divisor {
     }
 };
 
+template <bool LIFT>
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Divisor& d)
 {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
+        Two t(v[2 * i], v[2 * i + 1]);
+        if (LIFT) t = mul2(t, Two(kLift, kLift));
         float2 r;
-        d(Two(v[2 * i], v[2 * i + 1])).get(r.x, r.y);
+        d(t).get(r.x, r.y);
         w[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
     }
     return make_uint2(w[0], w[1]);
+}
+// (Two bodies: the lift as predicated instructions took 30 us beside 528 for
+// 64 x 4096 x 4096 weights.)
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const Divisor& d)
+{
+    return d.lift ? codes8<true>(v, d) : codes8<false>(v, d);
 }
 
 // A CTA takes 16 rows by BPT block columns at a time: half a warp per row

@@ -663,6 +663,26 @@ def test_quantize_special_values():
     assert not bool(torch.isnan(v[4, 128:]).any()) and bool(torch.isnan(v[5, 128:]).all())
 
 
+@pytest.mark.parametrize("exponent", [-98, 0, 120])
+def test_quantize_divides_exactly_for_every_significand(exponent):
+    """Block maxima of all 2^23 significands, the other values on and one step beside the midpoints of two
+    codes, where a quotient off by its last bit changes the code.  (A quotient rounded to 53 bits and then
+    to 24 is the one rounded to 24 at once, as 53 >= 2 * 24 + 2.)"""
+    n = 1 << 21
+    mid = torch.tensor([2.0 ** -10, 1.0625, 17.0, 232.0, 432.0], dtype=F64, device=DEV)
+    step = torch.tensor([-1, 0, 1], dtype=torch.int32, device=DEV)
+    q, s = torch.empty(n, 16, dtype=F8, device=DEV), torch.empty(1, n, device=DEV)
+    for first in range(0, 1 << 23, n):
+        m = torch.ldexp(1 + torch.arange(first, first + n, device=DEV).to(F64) / (1 << 23),
+                        torch.tensor(exponent, device=DEV)).to(F32)
+        sr = (m.to(F64) / 448).to(F32)
+        near = (sr.to(F64)[:, None] * mid).to(F32).view(torch.int32)
+        x = torch.cat([m[:, None], (near[:, :, None] + step).view(n, 15).view(F32)], 1)
+        A.moe_fp8_quantize_act(x, q, s)
+        assert torch.equal(s[0], sr)
+        assert torch.equal(q.to(F32), (x.to(F64) / sr.to(F64)[:, None]).to(F32).to(F8).to(F32))
+
+
 def test_quantize_slices_and_untouched_columns():
     g = gen(21)
     wide = torch.randn(33, 600, generator=g, device=DEV).to(BF)

@@ -9,10 +9,10 @@
 //
 // MANY rows an expert: rows are the tensor core's M, one tensor-memory lane
 // and one thread each, and 256 features its N: a thread's scale xs ws is then
-// one number for all of its columns, and an element costs one FMA.  (With rows
-// as N every column has its own scale, and reading those from shared memory
-// takes as long as the FMAs: 575 against 329 cycles for 128 x 256 elements, 16
-// warps.)
+// one number for all of its columns, and two elements cost one instruction
+// (0.51 us a block of a tile; one FMA an element, 0.53).  With rows as N every
+// column has its own scale, and reading those from shared memory takes as long
+// as the FMAs (575 against 329 cycles for 128 x 256 elements, 16 warps).
 // FEW: features are M and up to 32 rows N, as in grouped_gemm.cu, so that all
 // warps have work on a tile of one row and the MMAs compute 16 rows and not
 // 128: 120 W less at the same stream of weights, which the clock gets back.
@@ -100,6 +100,15 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
         o[0] = make_uint4(w[0], w[1], w[2], w[3]);
         o[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
+}
+
+// a += x s, b += y s: one instruction, two products.
+__device__ __forceinline__ void add2(float& a, float& b, uint32_t x, uint32_t y, float s)
+{
+    asm("{\n\t.reg .b64 p, q, t;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 t, {%4, %4};\n\t"
+        "fma.rn.f32x2 p, q, t, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x), "r"(y), "f"(s));
 }
 
 template <class CFG>
@@ -302,8 +311,8 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                                 wait_ld(d[(c / 16) & 1]);
                                 if (c + 16 < CW) tmem_ld16(src + c + 16, d[(c / 16 + 1) & 1]);
 #pragma unroll
-                                for (int j = 0; j < 16; j++)
-                                    acc[c + j] = fmaf(__uint_as_float(d[(c / 16) & 1][j]), s[g], acc[c + j]);
+                                for (int j = 0; j < 16; j += 2)
+                                    add2(acc[c + j], acc[c + j + 1], d[(c / 16) & 1][j], d[(c / 16) & 1][j + 1], s[g]);
                             }
                         }
                     }

@@ -47,7 +47,7 @@ using namespace tc;
 constexpr int kMaxStages = 12;
 constexpr int kStatic = 1024;        // bytes of static shared memory at most
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
-constexpr int kStaging = 4 * 2 * 4096;
+constexpr int kStaging = 8 * 4096;
 
 // Steps of 64 summed in one accumulator where the output is float32.  The
 // tensor core adds to its fp32 accumulator with truncation, so the relative
@@ -124,7 +124,9 @@ struct Units {
 };
 
 // A weight gradient's tiles: every expert's, an expert's feature tiles
-// fastest.  (A pair of CTAs gains it nothing: its way out takes longest.)
+// fastest.  (Pairs of CTAs took 99 us instead of 80 for 128 experts'
+// 768 x 2048 with 32 rows each, and 292 instead of 270 for 2048 x 1536 with
+// 256: the few steps of a tile do not hide the hand-overs across the pair.)
 template <int NB>
 struct Units<DW, NB, 1> {
     const Args& a;
@@ -207,55 +209,65 @@ __device__ __forceinline__ void add_row16(uint16_t* p, const uint32_t (&d)[16], 
 }
 
 // A warp's 32 rows of dW from row r0 on go out by TMA, 128 bytes of each at a
-// time, through two swizzled tiles in shared memory; zeros where `none`.
+// time, through swizzled tiles in shared memory; zeros where `none`.  Two
+// warps share the rows.  bf16: every other 128 bytes each, through a tile of
+// its own (one warp for all, with both tiles, took 194 us instead of 150 for
+// 128 experts' 2048 x 1536 with 32 rows each: reading the accumulators and
+// packing them was the longest way; with 256 rows each 270 either way).
+// float32: the first warp takes all, with both tiles (170 us with both warps,
+// 146 so, for 128 experts' 768 x 2048 with 32 rows each).
 __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap& out, const Unit& v, unsigned char* tiles,
-                                           int& turn, uint32_t src, int r0, bool none, bool add)
+                                           int& tile, uint32_t src, int r0, int group, bool none, bool add)
 {
     const int lane = threadIdx.x & 31, w = a.out_f32 ? 32 : 64;
-    for (int c = 0; c < v.n; c += w, turn ^= 1) {
-        unsigned char* tile = tiles + 4096 * turn;
-        if (lane == 0) bulk_wait_read<1>();   // its previous rows are on their way
-        __syncwarp();
-        for (int h = 0; h < w / 32; h++) {
-            uint32_t d[32];
-            if (none) {
+    if (a.out_f32 && group) return;
+    for (int c = group * w; c < v.n; c += a.out_f32 ? w : 2 * w) {
+        uint32_t d[32], e[32];   // 32 float32 values; 64 bf16 ones packed in d
+        auto load = [&](int from, uint32_t (&v)[32]) {
+            tmem_ld16(src + from, v);
+            tmem_ld16(src + from + 16, v + 16);
+            wait_ld(v);
+            hold16(v + 16);
+        };
+        if (none) {
 #pragma unroll
-                for (int j = 0; j < 32; j++) d[j] = 0;
-            } else {
-                tmem_ld16(src + c + 32 * h, d);
-                tmem_ld16(src + c + 32 * h + 16, d + 16);
-                wait_ld(d);
-                hold16(d + 16);
-            }
-            unsigned char* row = tile + 128 * lane;
-            if (a.out_f32) {
+            for (int j = 0; j < 32; j++) d[j] = 0;
+        } else {
+            load(c, d);
+            if (!a.out_f32) {
+                load(c + 32, e);
 #pragma unroll
-                for (int j = 0; j < 8; j++)
-                    *reinterpret_cast<uint4*>(row + 16 * (j ^ (lane & 7))) =
-                        make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
-            } else {
+                for (int j = 0; j < 16; j++) d[j] = pack_bf16(d[2 * j], d[2 * j + 1]);
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    *reinterpret_cast<uint4*>(row + 16 * ((j + 4 * h) ^ (lane & 7))) =
-                        make_uint4(pack_bf16(d[8 * j], d[8 * j + 1]), pack_bf16(d[8 * j + 2], d[8 * j + 3]),
-                                   pack_bf16(d[8 * j + 4], d[8 * j + 5]), pack_bf16(d[8 * j + 6], d[8 * j + 7]));
+                for (int j = 0; j < 16; j++) d[16 + j] = pack_bf16(e[2 * j], e[2 * j + 1]);
             }
         }
+        if (lane == 0) {   // the tile's previous rows are on their way
+            if (a.out_f32) bulk_wait_read<1>();
+            else bulk_wait_read<0>();
+        }
+        __syncwarp();
+        unsigned char* row = tiles + 4096 * tile + 128 * lane;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            *reinterpret_cast<uint4*>(row + 16 * (j ^ (lane & 7))) =
+                make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-            if (add) tma_add_3d(&out, smem_u32(tile), v.c0 + c, r0, v.e);
-            else tma_store_3d(&out, smem_u32(tile), v.c0 + c, r0, v.e);
+            if (add) tma_add_3d(&out, smem_u32(tiles + 4096 * tile), v.c0 + c, r0, v.e);
+            else tma_store_3d(&out, smem_u32(tiles + 4096 * tile), v.c0 + c, r0, v.e);
             bulk_commit();
         }
+        if (a.out_f32) tile ^= 1;   // (the next call goes on from here)
     }
 }
 
 // SUMS: row products summed up in the epilogue's registers, for float32 outputs
 // and for an inner index split over a cluster.
-template <int NB, bool SUMS>
+template <int MODE, int NB, bool SUMS>
 struct Epilogue {
-    static constexpr int WARPS = SUMS && NB > 32 ? 8 : 4;
+    static constexpr int WARPS = MODE == DW || (SUMS && NB > 32) ? 8 : 4;
     static constexpr int THREADS = 128 + 32 * WARPS;
     static constexpr int CW = NB / (WARPS / 4);        // columns of one warp
     static constexpr bool SPLIT = SUMS && CW > 64;     // registers moved from the control warps
@@ -263,7 +275,7 @@ struct Epilogue {
 static_assert(128 * kControlRegs + 256 * kSumRegs <= 384 * kRegs, "a larger split never starts");
 
 template <int MODE, int NB, int CG, bool SUMS>
-__global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
+__global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
     gg_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
               const __grid_constant__ CUtensorMap tm_out, const Args a)
 {
@@ -271,7 +283,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
     constexpr uint32_t TMEM = 2 * NB;
     constexpr bool RELAY = MODE == DW || CG == 2;
     constexpr bool PAIR = CG == 2;
-    using EPI = Epilogue<NB, SUMS>;
+    using EPI = Epilogue<MODE, NB, SUMS>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
     __shared__ uint32_t s_tmem;
@@ -279,7 +291,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
     __shared__ int s_abort, s_live;
     __shared__ long long s_scan[EPI::WARPS];
     unsigned char* ring = smem_raw;
-    unsigned char* staging = ring + (size_t)a.stages * STAGE;   // DW: 4 warps x 2 tiles of 32 rows x 128 bytes
+    unsigned char* staging = ring + (size_t)a.stages * STAGE;   // DW: two tiles of 32 rows x 128 bytes per lane quarter
     PlanExpert* tab = reinterpret_cast<PlanExpert*>(staging + (MODE == DW ? kStaging : 0));
     int* off = reinterpret_cast<int*>(tab);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
         tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);   // (not before: it may wait for what the kernel before holds)
     } else if (warp >= 4) {
         if constexpr (MODE == DW)
-            for (int i = tid - 128; i <= a.E; i += 128) off[i] = __ldg(a.offsets + i);
+            for (int i = tid - 128; i <= a.E; i += 32 * EPI::WARPS) off[i] = __ldg(a.offsets + i);
         else
             build_plan<32 * EPI::WARPS>(a.offsets, a.E, a.rows, {NB}, tab, s_scan, &s_live);
     }
@@ -463,14 +475,14 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
         // ============ epilogue: lane quarter q = warp % 4, one feature per thread; SUMS: columns
         // from cw on, CW of them
         const int q = warp & 3;
-        int it = 0, turn = 0;
+        int it = 0, tile = warp >= 8;   // DW: its staging tile
         bool ok = true, reduced = false;
         while (ok && units.next(v)) {
             const int f = v.m0 + 32 * q + lane;
             const bool mine = f < a.M;
             const bool none = MODE == DW && v.steps == 0;   // an expert without rows: its gradient is zero
             if (none && a.accumulate) continue;
-            const int cw = EPI::CW * ((warp - 4) >> 2);
+            const int cw = EPI::CW * ((warp - 4) >> 2), c1 = min(v.n, cw + EPI::CW);
             float sum[SUMS ? EPI::CW : 1];
             if (SUMS) {
 #pragma unroll
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                     if (a.direct) {
                         // a thread's feature is a row of dW: 16 adjacent columns at a time
                         const int64_t at = ((int64_t)v.e * a.M + f) * a.N + v.c0;
-                        for (int c = 0; c < v.n; c += 16) {
+                        for (int c = cw; c < c1; c += 16) {
                             uint32_t d[16];
                             tmem_ld16(src + c, d);
                             wait_ld(d);
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(Epilogue<NB, SUMS>::THREADS, 1)
                         }
                     } else if (v.m0 + 32 * q < a.M) {
                         if (s > 0 && lane == 0) bulk_wait();   // the partial sums before are in place
-                        store_tile(a, tm_out, v, staging + 8192 * q, turn, src, v.m0 + 32 * q, none, add);
+                        store_tile(a, tm_out, v, staging + 8192 * q, tile, src, v.m0 + 32 * q, (warp - 4) >> 2, none, add);
                     }
                 } else if constexpr (SUMS) {
 #pragma unroll
@@ -563,7 +575,7 @@ int launch(Args& a, int64_t tiles, int sms, int dev, const CUtensorMap& ta, cons
            cudaStream_t st)
 {
     constexpr int STAGE = kABytes + NB / CG * 128;
-    using EPI = Epilogue<NB, SUMS>;
+    using EPI = Epilogue<MODE, NB, SUMS>;
     static std::atomic<int> smem_set[kMaxDevices];
     auto* kern = gg_kernel<MODE, NB, CG, SUMS>;
     if (int rc = allow_smem(kern, kSmemMax - kStatic, smem_set, dev)) return rc;

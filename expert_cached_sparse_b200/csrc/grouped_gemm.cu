@@ -52,11 +52,14 @@ constexpr int kStaging = 8 * 4096;
 // Steps of 64 summed in one accumulator where the output is float32.  The
 // tensor core adds to its fp32 accumulator with truncation, so the relative
 // error of a sum grows by about 1e-6 for every 1000 inner indices; partial
-// sums of 512 are added up outside it, rounded to nearest: in registers (FWD,
-// DX: adding them to the output took 474 us instead of 208 where a tile has
-// eight of them) or in the output (DW: few experts have several).  bf16
-// outputs round to 2^-9 anyway: one accumulator for the whole sum.
-constexpr int kPartial = 8;
+// sums are added up outside it, rounded to nearest.  FWD, DX: of 256 inner
+// indices, in registers (2.4e-7 off, less than fp32 sums by FMAs from 1000
+// inner indices on; of 512, 4.7e-7 and 0 to 13% faster, 128, 1.5e-7 and
+// 5 to 17% slower; adding them to the output took 474 us instead of 208 where a tile
+// has eight of them).  DW: of 512 rows, in the output (few experts have
+// several).  bf16 outputs round to 2^-9 anyway: one accumulator for the whole
+// sum.
+constexpr int kPartial = 4, kPartialDw = 8;
 
 // Registers a thread of the control warps and of the epilogue's where the
 // latter hold 128 float32 sums each: together what the block is launched with,
@@ -760,7 +763,7 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     a.ldo = in;
     a.out_f32 = dw_dtype == MOE_DT_F32;
     a.accumulate = accumulate ? 1 : 0;
-    a.partial = a.out_f32 ? kPartial : 1 << 30;
+    a.partial = a.out_f32 ? kPartialDw : 1 << 30;
     a.E = experts;
     a.rows = rows;
     a.M = out;

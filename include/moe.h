@@ -524,10 +524,11 @@ int moe_act_terms(const void* d_x, int32_t x_dtype, int32_t rows, int32_t K, int
  *    may overlap an input;
  *  - products are summed in fp32 and rounded once to the output type
  *    (float32 or bf16, nearest even); the tensor core truncates as it adds, so
- *    float32 results are off by up to about 5e-7 relative (2-norm).  The same
- *    inputs give the same bits on every call.  No workspace, nothing read
- *    back: every call can be captured in a CUDA graph, and calls on different
- *    streams may overlap.
+ *    float32 results are off by about 3e-7 relative (2-norm), weight gradients
+ *    of experts with more than 256 rows by up to 5e-7.  The same inputs give
+ *    the same bits on every call.  No workspace, nothing read back: every call
+ *    can be captured in a CUDA graph, and calls on different streams may
+ *    overlap.
  * Errors: MOE_ERR_INVALID_ARG for bad sizes, types, alignments or NULL
  * pointers, MOE_ERR_UNSUPPORTED for sizes above the limits.
  * Pages: experts found in VRAM execute on the GPU ("FreeToken quantization",

@@ -484,11 +484,11 @@ struct PlanTile {
 struct PlanWalk {
     const PlanExpert* tab;
     const RowBlocks B;
-    int live, mt, i, parts;
+    int live, mt, i, parts, span;
     long long u, total;
 
     __device__ PlanWalk(const PlanExpert* t, int live_, const RowBlocks& b, int mt_, int part, int parts_)
-        : tab(t), B(b), live(live_), mt(mt_), i(0), parts(parts_), u(part), total((long long)t[live_].pre * mt_)
+        : tab(t), B(b), live(live_), mt(mt_), i(0), parts(parts_), span(parts_ / mt_ + 1), u(part), total((long long)t[live_].pre * mt_)
     {
     }
     // This CTA's share [lo, hi) of `steps` steps of the inner index, with the index split over
@@ -506,7 +506,7 @@ struct PlanWalk {
     __device__ __forceinline__ bool next(PlanTile& v)
     {
         if (u >= total) return false;
-        int hi = min(live - 1, i + parts);   // every expert has a tile at least
+        int hi = min(live - 1, i + span);   // every expert has mt tiles at least
         while (i < hi) {                     // the last expert whose first tile is at most u
             const int mid = (i + hi + 1) >> 1;
             if ((long long)tab[mid].pre * mt <= u) i = mid;
@@ -514,19 +514,22 @@ struct PlanWalk {
         }
         const PlanExpert x = tab[i];
         const long long r = u - (long long)x.pre * mt;
-        const int nt = B.blocks(x.r1 - x.r0);
-        int m, t = 0;
-        if (nt == 1) m = (int)r;
-        else if (r < 0x7fffffff) {   // a 64-bit division takes hundreds of cycles
+        u += parts;
+        const int n = x.r1 - x.r0, nt = B.blocks(n);
+        if (nt == 1) {   // no divisions: a small tile is not much longer than they take
+            v = {x.e, (int)r, x.r0, n};
+            return true;
+        }
+        int m, t;
+        if (r < 0x7fffffff) {   // a 64-bit division takes hundreds of cycles
             m = (int)r / nt;
             t = (int)r - m * nt;
         } else {
             m = (int)(r / nt);
             t = (int)(r % nt);
         }
-        const int share = B.share(x.r1 - x.r0), r0 = x.r0 + t * share;
+        const int share = B.share(n), r0 = x.r0 + t * share;
         v = {x.e, m, r0, min(share, x.r1 - r0)};
-        u += parts;
         return true;
     }
 };

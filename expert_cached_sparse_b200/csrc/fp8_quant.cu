@@ -313,8 +313,10 @@ extern "C" int moe_fp8_quantize_act(const void* d_x, int32_t x_dtype, int64_t ld
     const int sms = sm_count();
     const bool wide = groups * ((kb + 3) / 4) >= 4 * sms;
     const int64_t want = groups * (wide ? (kb + 3) / 4 : kb);
-    if (want > 0x7fffffff - 8 * sms) return MOE_ERR_UNSUPPORTED;
-    const int grid = (int)(want < 8 * sms ? want : 8 * sms);
+    // CTAs of one item or few, so that they end together (8 an SM: 49 us
+    // instead of 46 for SwiGLU on 24576 x 2048)
+    if (want > 0x7fffffff - 64 * sms) return MOE_ERR_UNSUPPORTED;
+    const int grid = (int)(want < 64 * sms ? want : 64 * sms);
     const bool f32 = x_dtype == MOE_DT_F32;
     auto* kern = wide ? (f32 ? (swiglu ? quant_act_kernel<true, true, 4> : quant_act_kernel<true, false, 4>)
                              : (swiglu ? quant_act_kernel<false, true, 4> : quant_act_kernel<false, false, 4>))
@@ -336,8 +338,10 @@ extern "C" int moe_fp8_quantize_weight(const void* d_w, int32_t w_dtype, int32_t
     ProfScope ps(MOE_PROF_QUANT, st);
     prof_count(MOE_PROF_QUANT, 1);
     const int64_t blocks = (int64_t)experts * ((out + 127) / 128) * ((in + 127) / 128);
-    if (blocks > 0x7fffffff - 4096) return MOE_ERR_UNSUPPORTED;   // 35 TB of bf16
-    const int cap = sm_count() * (w_dtype == MOE_DT_F32 ? 2 : 4);
+    // CTAs of a few blocks, so that they end together (all of them resident at
+    // once: 527 us instead of 495 for 64 x 4096 x 4096; one block each: 503)
+    const int cap = sm_count() * (w_dtype == MOE_DT_F32 ? 64 : 128);
+    if (blocks > 0x7fffffff - cap) return MOE_ERR_UNSUPPORTED;   // 35 TB of bf16
     const int grid = (int)(blocks < cap ? blocks : cap);
     auto* kern = w_dtype == MOE_DT_F32 ? quant_weight_kernel<true> : quant_weight_kernel<false>;
     MOE_CUDA_TRY(launch_overlapped(kern, grid, 1, 256, 0, st, d_w, (int)blocks, (int)out, (int)in, d_q, d_s));

@@ -444,7 +444,7 @@ def moe_profile_enable(timing: bool) -> None:
 
 
 def moe_profile_read(reset: bool = False) -> dict:
-    """{kind: {"launches", "timed", "ms"}} for router/lookup/permute/ffn/combine/fill."""
+    """{kind: {"launches", "timed", "ms"}} for router/lookup/permute/ffn/combine/fill/gemm/quant."""
     arr = (L.MoeProf * len(L.PROF_KINDS))()
     check("moe_profile_read", L.lib.moe_profile_read(arr, len(L.PROF_KINDS), 1 if reset else 0))
     return {k: {"launches": arr[i].launches, "timed": arr[i].timed, "ms": arr[i].ms}

@@ -869,3 +869,59 @@ def test_an_fp8_layer_together():
     ref = torch.zeros(n, H, dtype=F64, device=DEV).index_add_(0, assign_of.long() // k,
                                                               tw.flatten()[assign_of.long()][:, None].double() * yy)
     assert float((out.double() - ref).norm() / ref.norm()) < 4 * 2.0 ** -4
+
+
+def test_products_behind_the_fused_ffn_wait_for_it_and_are_profiled():
+    """A product and a quantiser launched right behind the fused FFN (whose kernels let the next one start
+    early) read all that it wrote.  (Rows are normalised once a turn: the FFN squares their size.)"""
+    E, k, H, F, n = 8, 2, 256, 192, 64
+    g = gen(31)
+    _, _, off, _, _, xp, _ = _route(n, E, k, H, g)
+    rows = n * k
+    shape = A.make_shape(1, E, H, F, k, A.W_BF16)
+
+    class Ew:
+        w13_scales = w2_scales = None
+        tensor_scales = np.zeros(2, np.float32)
+
+    pool = []
+    for e in range(E):
+        ew = Ew()
+        for name, s in (("w13", (2 * F, H)), ("w2", (H, F))):
+            w = (0.3 * torch.randn(s, generator=g, device=DEV)).to(BF)
+            setattr(ew, name, w.cpu().view(torch.int16).numpy().view(np.uint16))
+        pool.append(A.moe_pack_expert(shape, ew))
+    pool = torch.from_numpy(np.concatenate(pool)).to(DEV)
+    w = (0.1 * torch.randn(E, H, H, generator=g, device=DEV)).to(BF)
+    slots = torch.arange(E, dtype=torch.int32, device=DEV)
+    wsf = torch.empty(A.moe_ffn_workspace_bytes(shape, rows), dtype=torch.uint8, device=DEV)
+    x, y = torch.empty_like(xp), torch.empty_like(xp)
+    q, s = torch.empty(rows, H, dtype=F8, device=DEV), torch.empty(H // 128, rows, device=DEV)
+
+    def chain(pause):
+        x.copy_(xp)
+        for _ in range(8):
+            for f in (lambda: A.moe_grouped_ffn(shape, pool, E, slots, off, x, rows, y, wsf),
+                      lambda: A.moe_grouped_gemm(y, w, off, x),
+                      lambda: x.copy_(torch.nn.functional.layer_norm(x.float(), (H,))),
+                      lambda: A.moe_grouped_ffn(shape, pool, E, slots, off, x, rows, y, wsf),
+                      lambda: A.moe_fp8_quantize_act(y, q, s)):
+                f()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [t.clone() for t in (x, y, q.to(F32), s)]
+
+    want = chain(True)
+    assert bool(torch.isfinite(want[0]).all()) and bool(want[0].any())
+    A.moe_profile_enable(True)
+    try:
+        A.moe_profile_read(reset=True)
+        got = chain(False)
+        counts = A.moe_profile_read(reset=True)
+    finally:
+        A.moe_profile_enable(False)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert counts["gemm"]["launches"] == 8 and counts["quant"]["launches"] == 8 and counts["gemm"]["ms"] > 0
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))

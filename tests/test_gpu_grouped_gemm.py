@@ -899,29 +899,40 @@ def test_products_behind_the_fused_ffn_wait_for_it_and_are_profiled():
     q, s = torch.empty(rows, H, dtype=F8, device=DEV), torch.empty(H // 128, rows, device=DEV)
 
     def chain(pause):
+        st = torch.cuda.current_stream()
         x.copy_(xp)
         for _ in range(8):
-            for f in (lambda: A.moe_grouped_ffn(shape, pool, E, slots, off, x, rows, y, wsf),
-                      lambda: A.moe_grouped_gemm(y, w, off, x),
+            for f in (lambda: A.moe_grouped_ffn(shape, pool, E, slots, off, x, rows, y, wsf, stream=st),
+                      lambda: A.moe_grouped_gemm(y, w, off, x, stream=st),
                       lambda: x.copy_(torch.nn.functional.layer_norm(x.float(), (H,))),
-                      lambda: A.moe_grouped_ffn(shape, pool, E, slots, off, x, rows, y, wsf),
-                      lambda: A.moe_fp8_quantize_act(y, q, s)):
+                      lambda: A.moe_grouped_ffn(shape, pool, E, slots, off, x, rows, y, wsf, stream=st),
+                      lambda: A.moe_fp8_quantize_act(y, q, s, stream=st)):
                 f()
                 if pause:
                     torch.cuda.synchronize()
+
+    def results():
         torch.cuda.synchronize()
         return [t.clone() for t in (x, y, q.to(F32), s)]
 
-    want = chain(True)
+    chain(True)
+    want = results()
     assert bool(torch.isfinite(want[0]).all()) and bool(want[0].any())
     A.moe_profile_enable(True)
     try:
         A.moe_profile_read(reset=True)
-        got = chain(False)
+        chain(False)
+        got = results()
         counts = A.moe_profile_read(reset=True)
     finally:
         A.moe_profile_enable(False)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert counts["gemm"]["launches"] == 8 and counts["quant"]["launches"] == 8 and counts["gemm"]["ms"] > 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(False)
     for _ in range(3):
-        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+        for t in (x, y, s):
+            t.fill_(7)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))

@@ -76,8 +76,8 @@ struct Run8<true> {
     float4 a, b;
     __device__ __forceinline__ void load(const void* p)
     {
-        a = __ldg(static_cast<const float4*>(p));
-        b = __ldg(static_cast<const float4*>(p) + 1);
+        a = static_cast<const float4*>(p)[0];
+        b = static_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void forget() {}
     __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
@@ -91,7 +91,7 @@ struct Run8<true> {
 template <>
 struct Run8<false> {
     uint4 u;
-    __device__ __forceinline__ void load(const void* p) { u = __ldg(static_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const void* p) { u = *static_cast<const uint4*>(p); }
     // keeps the compiler from holding the widened values instead of the packed ones
     __device__ __forceinline__ void forget() { asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)); }
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
@@ -182,7 +182,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Divisor& d)
 // (eight columns a lane), all BPT loads in flight before the first block is
 // worked on.  The 16 rows' scales of a block column are adjacent.
 template <bool XF32, bool SWIGLU, int BPT>
-__global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__ x, int64_t ldx, int rows, int cols,
+__global__ void __launch_bounds__(256) quant_act_kernel(const void* x, int64_t ldx, int rows, int cols,
                                                         uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
 {
     constexpr int SZ = XF32 ? 4 : 2;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const void* __restrict__
 // between the maximum and the codes, so the block is read once.
 template <bool XF32>
 __global__ void __launch_bounds__(256, XF32 ? 2 : 4)
-    quant_weight_kernel(const void* __restrict__ w, int blocks, int out, int in, uint8_t* __restrict__ q,
+    quant_weight_kernel(const void* w, int blocks, int out, int in, uint8_t* __restrict__ q,
                         float* __restrict__ s)
 {
     __shared__ float s_m[2][8];

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
         tmem_alloc<CG>(smem_u32(&s_tmem), TMEM);   // (not before: it may wait for what the kernel before holds)
     } else if (warp >= 4) {
         if constexpr (MODE == DW)
-            for (int i = tid - 128; i <= a.E; i += 32 * EPI::WARPS) off[i] = __ldg(a.offsets + i);
+            for (int i = tid - 128; i <= a.E; i += 32 * EPI::WARPS) off[i] = a.offsets[i];
         else
             build_plan<32 * EPI::WARPS>(a.offsets, a.E, a.rows, {NB}, tab, s_scan, &s_live);
     }

@@ -84,7 +84,7 @@ __device__ __forceinline__ float fetch_f32(const float* p, bool in)
 {
     float v;
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
-                 "@p ld.global.nc.f32 %0, [%1];\n\t}" : "=f"(v) : "l"(p), "r"((int)in));
+                 "@p ld.global.f32 %0, [%1];\n\t}" : "=f"(v) : "l"(p), "r"((int)in));
     return v;
 }
 

@@ -9,7 +9,10 @@ namespace moe {
 // before it has called start_next() in every CTA, or ended.  Until
 // wait_before() returns that kernel may still run; every thread calls it
 // before anything reads or writes global memory.  Every such kernel waits, so a
-// kernel that has ended means that all before it have.  (quantise, e4m3
+// kernel that has ended means that all before it have.  Loads of what that
+// kernel may write are plain ones through plain pointers: __ldg, ld.global.nc
+// and const __restrict__ parameters promise that nothing writes the data while
+// this kernel runs, and let the compiler move the load ahead of the wait.  (quantise, e4m3
 // product, SwiGLU quantise, e4m3 product of one token, 128 experts, 2048 x 768:
 // 18.9 us in a graph against 20.7 without.)
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -418,10 +418,10 @@ struct RowBlocks {
 };
 
 // Rows of expert e; none for a range that no offsets of moe_permute hold.
-__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int rows, int& lo, int& hi)
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int rows, int& lo, int& hi)
 {
-    lo = __ldg(offsets + e);
-    hi = __ldg(offsets + e + 1);
+    lo = offsets[e];
+    hi = offsets[e + 1];
     if (lo < 0 || hi < lo || hi > rows) lo = hi = 0;
 }
 
@@ -434,7 +434,7 @@ __host__ __device__ static inline int plan_bytes(int E) { return (int)align_up(s
 // of the CTA has to follow.  Ranges that overlap so often that the blocks pass
 // 2^31 void the call.
 template <int NT>
-__device__ __forceinline__ void build_plan(const int32_t* __restrict__ offsets, int E, int rows, const RowBlocks& B,
+__device__ __forceinline__ void build_plan(const int32_t* offsets, int E, int rows, const RowBlocks& B,
                                            PlanExpert* tab, long long* scratch, int* live)
 {
     const int tid = threadIdx.x - (blockDim.x - NT), lane = tid & 31, warp = tid >> 5, nt = NT;

@@ -28,9 +28,9 @@
 // Roles, one persistent CTA or pair per SM or two: warps 0 and 2 copy the two
 // operands (one warp for both issued too slowly), warp 1 (of the pair's first
 // CTA) issues the MMAs into one of two accumulators, warps 4 on read the other
-// one back and store it.  Warp 3 works between copies and MMAs where that is
-// needed: it zeroes the surplus rows (DW) and tells the pair's first CTA that a
-// stage is in place (CG = 2).
+// one back and store it.  In DW warp 3 works between copies and MMAs: it zeroes
+// the surplus rows.  The copies of a pair's both CTAs complete on the first
+// one's barriers, where its MMA warp waits for them.
 // Every wait is bounded; a timeout records MOE_ERR_TIMEOUT, raises the CTA's
 // abort flag so that the other roles stop, and the CTA waits for its own
 // copies and MMAs before it returns.
@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
 {
     constexpr int STAGE = kABytes + NB / CG * 128;
     constexpr uint32_t TMEM = 2 * NB;
-    constexpr bool RELAY = MODE == DW || CG == 2;
     constexpr bool PAIR = CG == 2;
     using EPI = Epilogue<MODE, NB, SUMS>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -310,8 +309,8 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < a.stages; i++) {
-            mbar_init(smem_u32(&full[i]), 2);   // both copy warps
-            mbar_init(smem_u32(&ready[i]), CG);
+            mbar_init(smem_u32(&full[i]), 2 * CG);   // both copy warps
+            mbar_init(smem_u32(&ready[i]), 1);       // DW
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -342,37 +341,38 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
     const uint32_t tmem = s_tmem;
     Units<MODE, NB, CG> units(a, tab, off, MODE == DW ? 0 : s_live, rank);
     Unit v;
+    const uint32_t full0 = PAIR ? peer_addr(smem_u32(full), 0) : smem_u32(full);
 
     if (warp < 4) {
         if (EPI::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (warp == 0) {
             // ============ copies of the features (A)
             if (elect1())
-                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
+                copy_loop<STAGE, CG>(full0, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
                                  [&] { return units.next(v) ? v.steps : -1; },
                                  [&](int s, uint32_t bar, uint32_t sa, int) {
                                      const int k = v.k0 + 64 * s;
-                                     mbar_expect_tx(bar, kABytes);
+                                     mbar_expect_tx<CG>(bar, kABytes);
                                      if (MODE == FWD) {
-                                         tma_3d(sa, &tm_a, k, v.m0, v.e, bar);
+                                         tma_3d<CG>(sa, &tm_a, k, v.m0, v.e, bar);
                                      } else if (a.chunks_a) {
-                                         if (MODE == DX) tma_4d(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
+                                         if (MODE == DX) tma_4d<CG>(sa, &tm_a, 0, k, v.m0 / 64, v.e, bar);
                                          else tma_3d(sa, &tm_a, 0, k, v.m0 / 64, bar);
                                      } else
                                          for (int i = 0; i < 2; i++) {
-                                             if (MODE == DX) tma_3d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, v.e, bar);
+                                             if (MODE == DX) tma_3d<CG>(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, v.e, bar);
                                              else tma_2d(sa + 8192 * i, &tm_a, v.m0 + 64 * i, k, bar);
                                          }
                                  });
             __syncwarp();
             start_next();   // (at the kernel's start: the same within 1%, and SMs held for longer)
-            drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
+            if (!PAIR) drain_copies(full, a.stages, s_copy, 0, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 2) {
             // ============ copies of the columns (B)
             if (elect1()) {
                 int ub = 0;
                 uint32_t bytes = 0;
-                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
+                copy_loop<STAGE, CG>(full0, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
                                  [&] {
                                      if (!units.next(v)) return -1;
                                      ub = MODE == DW ? (a.chunks_b ? NB / 64 : (v.n + 63) / 64) : row_units(v.nb, a.box);
@@ -382,13 +382,9 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                                  [&](int s, uint32_t bar, uint32_t sa, int) {
                                      const int k = v.k0 + 64 * s;
                                      const uint32_t sb = sa + kABytes;
-                                     if (PAIR && bytes == 0) {   // a pair's second half without columns
-                                         mbar_arrive(bar);
-                                         return;
-                                     }
-                                     mbar_expect_tx(bar, bytes);
+                                     mbar_expect_tx<CG>(bar, bytes);   // (none: a pair's second half without columns)
                                      if (MODE != DW)
-                                         tma_rows(sb, tm_b, k, v.cb, ub, a.box, bar);
+                                         tma_rows<CG>(sb, tm_b, k, v.cb, ub, a.box, bar);
                                      else if (a.chunks_b)
                                          tma_3d(sb, &tm_b.m[0], 0, k, v.cb / 64, bar);
                                      else
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                                  });
             }
             __syncwarp();
-            drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
+            if (!PAIR) drain_copies(full, a.stages, s_copy, 1, a.withhold && blockIdx.x == 0, err);
         } else if (warp == 1) {
             // ============ MMAs
             if (!PAIR || rank == 0) {
@@ -413,13 +409,13 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                             if (first) {
                                 const int ab = it & 1;
                                 if (it >= 2 &&   // the epilogue has read what this accumulator held
-                                    !(ok = mbar_wait(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
+                                    !(ok = mbar_wait<CG>(smem_u32(&acc_empty[ab]), ((it >> 1) - 1) & 1, abort_v, a.wait, err)))
                                     break;
                                 d = tmem + (uint32_t)(ab * NB);
                                 left = min(a.partial, v.steps - s);
                             }
-                            const uint32_t bar = smem_u32(RELAY ? &ready[st] : &full[st]);
-                            if (!(ok = mbar_wait(bar, ph, abort_v, a.wait, err))) break;
+                            const uint32_t bar = smem_u32(MODE == DW ? &ready[st] : &full[st]);
+                            if (!(ok = mbar_wait<CG>(bar, ph, abort_v, a.wait, err))) break;
                             fence_after();
                             const uint32_t sa = smem_u32(ring + (size_t)st * STAGE), sb = sa + kABytes;
                             const uint64_t da = MODE == FWD ? desc_k(sa) : desc_mn(sa, 8192);
@@ -440,20 +436,20 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                         }
                     }
                     commit<CG>(smem_u32(&fin));   // every MMA completes before tensor memory is released
-                    mbar_drain(smem_u32(&fin), 0, err);
+                    mbar_drain<CG>(smem_u32(&fin), 0, err);
                 }
                 __syncwarp();
             }
         } else if (warp == 3) {
             // ============ between copies and MMAs
-            if (RELAY) {
+            if (MODE == DW) {
                 int st = 0;
                 uint32_t ph = 0;
                 bool ok = true;
                 while (ok && units.next(v)) {
                     for (int s = 0; s < v.steps; s++) {
                         if (!(ok = mbar_wait_warp(smem_u32(&full[st]), ph, abort_v, a.wait, err))) break;
-                        if (MODE == DW && s == v.steps - 1 && (v.tail & 15)) {
+                        if (s == v.steps - 1 && (v.tail & 15)) {
                             // zero the surplus rows of the last 16-row step in every 64-column chunk of both operands
                             unsigned char* p = ring + (size_t)st * STAGE + 128 * v.tail;
                             const int z = 128 * (16 - (v.tail & 15)), chunks = 2 + (v.nh + 63) / 64;
@@ -463,10 +459,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                             asm volatile("fence.proxy.async;" ::: "memory");
                             __syncwarp();
                         }
-                        if (lane == 0) {
-                            if (PAIR) mbar_arrive_cluster(peer_addr(smem_u32(&ready[st]), 0));
-                            else mbar_arrive(smem_u32(&ready[st]));
-                        }
+                        if (lane == 0) mbar_arrive(smem_u32(&ready[st]));
                         if (++st == a.stages) { st = 0; ph ^= 1; }
                     }
                 }
@@ -496,7 +489,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                 const int ab = it & 1;
                 const bool add = s > 0 || (MODE == DW && a.accumulate);   // to what is there
                 if (!none) {
-                    if (!(ok = mbar_wait_warp(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+                    if (!(ok = mbar_wait_warp<CG>(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
                     fence_after();
                 }
                 const uint32_t src = tmem + (uint32_t)(ab * NB) + ((uint32_t)(32 * q) << 16);
@@ -565,12 +558,18 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
     }
     fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();   // nothing of the peer reads this CTA's shared or tensor memory any more
+    if (PAIR) {
+        cluster_sync();   // the roles of both CTAs have ended
+        if (rank == 0 && tid == 0 && (s_abort || ld_cluster(peer_addr(smem_u32(&s_abort), 1))))
+            drain_pair(full, a.stages, s_copy, a.withhold && blockIdx.x == 0, err);
+        if (rank == 1 && warp == 1) mbar_drain<CG>(smem_u32(&fin), 0, err);   // the commits' arrivals here
+        __syncwarp();
+    }
     if (warp == 1) {
         fence_after();
         tmem_dealloc<CG>(tmem, TMEM);
     }
-    if (PAIR) cluster_sync();
+    if (PAIR) cluster_sync();   // nothing of the peer reads or arrives in this CTA's memory any more
 }
 
 template <int MODE, int NB, int CG, bool SUMS>

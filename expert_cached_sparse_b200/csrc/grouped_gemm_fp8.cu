@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
                 // depend on them, but the tensor core's power does, and with it the clock.
                 int u = 0;
                 uint64_t tall = ~0ull;   // per stage, 4 bits: boxes that may hold something, less one
-                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[0],
+                copy_loop<STAGE, 1>(smem_u32(full), empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0,
+                                 err, &s_copy[0],
                                  [&] {
                                      if (!tiles.next(v)) return -1;
                                      u = row_units(v.n, a.box);
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(CFG::THREADS, 1)
         } else if (warp == 2) {
             // ============ copies of the weights
             if (elect1())
-                copy_loop<STAGE>(full, empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0, err, &s_copy[1],
+                copy_loop<STAGE, 1>(smem_u32(full), empty, ring, a.stages, abort_v, a.wait, a.withhold && blockIdx.x == 0,
+                                 err, &s_copy[1],
                                  [&] { return tiles.next(v) ? bhi - blo : -1; },
                                  [&](int s, uint32_t bar, uint32_t sa, int) {
                                      mbar_expect_tx(bar, WEIGHTS);

@@ -46,14 +46,24 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// One arrival by the calling lane on a barrier anywhere in the cluster, with
-// no ordering of the thread's own writes (a release there is a memory barrier
-// of about a thousand cycles).  What it announces is already in place: copies
-// whose completion the thread has seen, accumulators read.  Callers with
-// writes of their own to publish fence first.
+// One arrival by the calling lane on a barrier anywhere in the cluster: what it
+// and the lanes of its warp did before is done for whoever waits there with an
+// acquire at cluster scope (mbar_try<2>).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ long long ld_cluster64(uint32_t addr)
+{
+    long long v;
+    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v)
@@ -97,35 +107,54 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// An arrival that announces `bytes` of copies.  CG = 2: on a barrier of the
+// pair's first CTA, from either.  It publishes nothing itself, so it is a
+// relaxed one: the copies' own completion on the barrier is a release at
+// cluster scope.
+template <int CG = 1>
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
+    if (CG == 1)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+    else
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                     : "memory");
 }
 // One arrival by the calling lane.
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// CG = 2: a barrier of this CTA on which the pair's other CTA, or work issued
+// there, arrives too, so the acquire is one at cluster scope.
+template <int CG = 1>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
+    if (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
     return ok != 0;
 }
 // Bounded wait: false when another role raised the CTA's abort flag, or after
 // `limit` cycles, in which case it raises the flag itself and records
 // MOE_ERR_TIMEOUT in *error.
+template <int CG = 1>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit,
                                           int* error)
 {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<CG>(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
+    while (!mbar_try<CG>(bar, parity)) {
         if (*abort_flag) return false;
         if (clock64() - t0 > limit) {
             *abort_flag = 1;
@@ -136,17 +165,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 // The same for a converged warp: every lane gets the same answer.
+template <int CG = 1>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit,
                                                int* error)
 {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, error));
+    return __all_sync(0xffffffffu, mbar_wait<CG>(bar, parity, abort_flag, limit, error));
 }
 // Drain wait for this CTA's own copies or MMAs before it exits: bounded by
 // time only.
+template <int CG = 1>
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, int* error)
 {
     const long long t0 = clock64();
-    while (!mbar_try(bar, parity))
+    while (!mbar_try<CG>(bar, parity))
         if (clock64() - t0 > kWaitCycles) {
             atomicCAS(error, 0, (int)MOE_ERR_TIMEOUT);
             return;
@@ -158,24 +189,34 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* m)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
+// Copies into this CTA's shared memory.  CG = 2: their barrier may be the
+// other CTA's of the pair (`bar` a cluster address).
+#define MOE_TC_LOAD(dim, coords, ...)                                                                             \
+    do {                                                                                                          \
+        if (CG == 1)                                                                                              \
+            asm volatile("cp.async.bulk.tensor." dim ".shared::cluster.global.tile.mbarrier::complete_tx::bytes " \
+                         "[%0], [%1, " coords "], [%2];" ::"r"(dst), "l"(m), "r"(bar), __VA_ARGS__ : "memory");   \
+        else                                                                                                      \
+            asm volatile("cp.async.bulk.tensor." dim ".shared::cluster.global.tile.mbarrier::complete_tx::bytes"  \
+                         ".cta_group::2 "                                                                         \
+                         "[%0], [%1, " coords "], [%2];" ::"r"(dst), "l"(m), "r"(bar), __VA_ARGS__ : "memory");   \
+    } while (0)
+template <int CG = 1>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+    MOE_TC_LOAD("2d", "{%3, %4}", "r"(x), "r"(y));
 }
+template <int CG = 1>
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
-                 : "memory");
+    MOE_TC_LOAD("3d", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
 }
-
+template <int CG = 1>
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-                 : "memory");
+    MOE_TC_LOAD("4d", "{%3, %4, %5, %6}", "r"(x), "r"(y), "r"(z), "r"(w));
 }
+#undef MOE_TC_LOAD
 // Stores of a converged warp's own tiles: ordered by one lane's bulk groups,
 // so commit and wait run on lane 0, which issues.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z)
@@ -203,10 +244,11 @@ struct CopyPos {
 };
 // A copy warp's loop over the stages of its tiles, walked by one thread:
 // next() gives the steps of the next tile or -1, issue(s, bar, address, stage)
-// starts the copies of step s and announces their bytes on the stage's barrier.
+// starts the copies of step s and announces their bytes on the stage's barrier
+// (`full`: the address of the first one; CG = 2: in the pair's first CTA).
 // `withheld`: the first stage is never filled (a test's doing).
-template <int STAGE, class NEXT, class ISSUE>
-__device__ __forceinline__ void copy_loop(uint64_t* full, uint64_t* empty, unsigned char* ring, int stages,
+template <int STAGE, int CG, class NEXT, class ISSUE>
+__device__ __forceinline__ void copy_loop(uint32_t full, uint64_t* empty, unsigned char* ring, int stages,
                                           volatile int* abort_flag, long long limit, bool withheld, int* error,
                                           volatile CopyPos* end, NEXT next, ISSUE issue)
 {
@@ -216,9 +258,9 @@ __device__ __forceinline__ void copy_loop(uint64_t* full, uint64_t* empty, unsig
     bool ok = true;
     while (ok && (steps = next()) >= 0)
         for (int s = 0; s < steps; s++) {
-            if (!(ok = mbar_wait(smem_u32(&empty[st]), ph ^ 1, abort_flag, limit, error))) break;
+            if (!(ok = mbar_wait<CG>(smem_u32(&empty[st]), ph ^ 1, abort_flag, limit, error))) break;
             if (withheld) withheld = false;
-            else issue(s, smem_u32(&full[st]), smem_u32(ring) + (uint32_t)(st * STAGE), st);
+            else issue(s, full + 8 * st, smem_u32(ring) + (uint32_t)(st * STAGE), st);
             issued++;
             if (++st == stages) { st = 0; ph ^= 1; }
         }
@@ -244,6 +286,27 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, volatil
     if (mine == 0)   // stage i was last filled in this pass over the ring if i < st, else in the previous one
         for (int i = 0; i < stages && i < most; i++)
             if (!(withheld && i == 0)) mbar_drain(smem_u32(&full[i]), i < st ? ph : (ph ^ 1), error);
+}
+
+// The same for a pair of CTAs whose copies all complete on the first one's
+// barriers: called by one thread there when the copy warps and the MMAs of both
+// have ended and one of them gave up (otherwise the MMAs have waited for every
+// copy), before either CTA exits.
+__device__ __forceinline__ void drain_pair(uint64_t* full, int stages, CopyPos* end, bool withheld, int* error)
+{
+    long long n[4], most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        n[i] = ld_cluster64(peer_addr(smem_u32(&end[i & 1].issued), i >> 1));
+        most = max(most, n[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (withheld && i < 2 && n[i] > 0) mbar_arrive(smem_u32(&full[0]));
+        for (long long k = n[i]; k < most; k++) mbar_arrive(smem_u32(&full[k % stages]));
+    }
+    for (long long k = max(0ll, most - stages); k < most; k++)
+        mbar_drain<2>(smem_u32(&full[k % stages]), (uint32_t)(k / stages) & 1, error);
 }
 
 // ------------------------------------------------------------------ tcgen05
@@ -376,12 +439,13 @@ __device__ __forceinline__ int row_units(int n, int box)   // in boxes of the sm
     while (__popc(u) > 2) u += u & -u;
     return u;
 }
+template <int CG = 1>
 __device__ __forceinline__ void tma_rows(uint32_t dst, const RowMaps& maps, int x, int row, int units, int box,
                                          uint32_t bar)
 {
     for (int i = kRowMaps - 1; i >= 0; i--)
         if (units >> i & 1) {
-            tma_2d(dst, &maps.m[i], x, row, bar);
+            tma_2d<CG>(dst, &maps.m[i], x, row, bar);
             dst += (uint32_t)(128 * box << i);
             row += box << i;
         }

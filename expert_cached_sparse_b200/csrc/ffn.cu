@@ -45,7 +45,8 @@ constexpr long long kWaitCycles = 4000000000ll;   // ~2 s before a wait gives up
 // that each may start while the previous one drains; every kernel waits for
 // its predecessor's results (griddepcontrol.wait, a no-op for a normal
 // launch) before reading them, and lets its successor launch once all its
-// CTAs are running.
+// CTAs are running.  What the predecessor may write is read by plain loads
+// through plain pointers (overlap.cuh says why).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -126,12 +127,12 @@ size_t ffn_ws_layout(const moe_shape* s, int rows, void* base, FfnWs* w)
 // gather[r]/gk of the source).  With `groups` set, the last CTA writes the
 // per-expert token-group prefix and clears `zero`.
 template <bool IN_F32>
-__global__ void __launch_bounds__(kPrepThreads) ffn_prep_kernel(const void* __restrict__ in, int rows, int K,
+__global__ void __launch_bounds__(kPrepThreads) ffn_prep_kernel(const void* in, int rows, int K,
                                                                 uint16_t* __restrict__ out,
-                                                                const int32_t* __restrict__ offsets,
-                                                                const int32_t* __restrict__ slot_of, int E,
+                                                                const int32_t* offsets,
+                                                                const int32_t* slot_of, int E,
                                                                 int pool_slots, int32_t* __restrict__ groups,
-                                                                const int32_t* __restrict__ gather, int gk,
+                                                                const int32_t* gather, int gk,
                                                                 int32_t* __restrict__ zero, int nzero)
 {
     pdl_wait();
@@ -176,16 +177,16 @@ __global__ void __launch_bounds__(kPrepThreads) ffn_prep_kernel(const void* __re
     const int nblocks = gridDim.x - (groups ? 1 : 0);
     const int nch = K / 8;   // 8-element chunks per row
     for (int r = blockIdx.x; r < rows; r += nblocks) {
-        const size_t sr = gather ? (size_t)(__ldg(gather + r) / gk) : (size_t)r;   // source row
+        const size_t sr = gather ? (size_t)(gather[r] / gk) : (size_t)r;   // source row
         const float* inf = static_cast<const float*>(in) + sr * K;
         const uint16_t* inb = static_cast<const uint16_t*>(in) + sr * K;
         // two adjacent source columns (col even) as a bf16 pair
         auto pair = [&](int col) -> uint32_t {
             if (IN_F32) {
-                const float2 v = __ldg(reinterpret_cast<const float2*>(inf + col));
+                const float2 v = *reinterpret_cast<const float2*>(inf + col);
                 return (uint32_t)f32_to_bf16_bits(v.x) | ((uint32_t)f32_to_bf16_bits(v.y) << 16);
             }
-            return __ldg(reinterpret_cast<const uint32_t*>(inb + col));
+            return *reinterpret_cast<const uint32_t*>(inb + col);
         };
         for (int c = threadIdx.x; c < nch; c += kPrepThreads) {
             // output chunk cc of 64-column block kt holds, for j = 2(cc&1) + jj

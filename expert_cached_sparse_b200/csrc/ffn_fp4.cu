@@ -363,8 +363,8 @@ struct Fmt {
 // bytes of their operand images are summed in boffc (in expert order); and
 // group g's entry gtab[g] = {first row, rows, slot, per-chunk byte offset of
 // its operand image} lets the GEMM find a unit with one load.
-__global__ void __launch_bounds__(256) fp4_plan_kernel(const int32_t* __restrict__ offsets,
-                                                       const int32_t* __restrict__ slot_of, int E, int rows,
+__global__ void __launch_bounds__(256) fp4_plan_kernel(const int32_t* offsets,
+                                                       const int32_t* slot_of, int E, int rows,
                                                        int pool_slots, int NT, int T, int nsub,
                                                        int32_t* __restrict__ gpre, int32_t* __restrict__ boffc,
                                                        int4* __restrict__ gtab,
@@ -501,7 +501,8 @@ __device__ __noinline__ uint32_t term8(float* v, uint32_t* scode)
 
 // 8 activation values of a row (bf16 bits or fp32) as floats.  fp32 rows
 // may have been written earlier in the same kernel (h in the fused decode
-// kernel), so they are read through L2, not the read-only cache.
+// kernel), so they are read through L2.  bf16 rows may be a predecessor's that
+// this kernel overlaps: a plain load, not one through the read-only cache.
 template <bool IN_F32>
 __device__ __forceinline__ void load8(const void* row, int k, float (&v)[8])
 {
@@ -511,7 +512,7 @@ __device__ __forceinline__ void load8(const void* row, int k, float (&v)[8])
         const float4 b = __ldcg(reinterpret_cast<const float4*>(f) + 1);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k));
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k);
         const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int h = 0; h < 4; h++) {
@@ -564,9 +565,9 @@ constexpr int kSegCols = 8 * kQuantThreads;
 
 template <int WFMT, int T, bool IN_F32, bool CANON = false>
 __global__ void __launch_bounds__(kQuantThreads) fp4_terms_kernel(
-    const void* __restrict__ in, int rows, int K, const int32_t* __restrict__ gather, int gk,
-    const int32_t* __restrict__ offsets, const int32_t* __restrict__ slot_of, int E, int pool_slots,
-    const int32_t* __restrict__ boffc, int NT, char* __restrict__ bimg, int32_t* __restrict__ rex,
+    const void* in, int rows, int K, const int32_t* gather, int gk,
+    const int32_t* offsets, const int32_t* slot_of, int E, int pool_slots,
+    const int32_t* boffc, int NT, char* __restrict__ bimg, int32_t* __restrict__ rex,
     uint8_t* __restrict__ ccodes = nullptr, uint8_t* __restrict__ cscales = nullptr)
 {
     using FM = Fmt<WFMT>;
@@ -585,19 +586,18 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_terms_kernel(
             int lo = 0, hi = E - 1;   // expert of row r: the largest e with offsets[e] <= r
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (__ldg(offsets + mid) <= r) lo = mid;
+                if (offsets[mid] <= r) lo = mid;
                 else hi = mid - 1;
             }
-            const int e = lo, sl = __ldg(slot_of + e), m = __ldg(offsets + e + 1) - __ldg(offsets + e);
-            if (!(m > 0 && sl >= 0 && sl < pool_slots && __ldg(offsets + e) >= 0 && __ldg(offsets + e + 1) <= rows))
-                continue;
-            const int loc = r - __ldg(offsets + e), gi = loc / NT, nt = min(NT, m - gi * NT);
+            const int e = lo, sl = slot_of[e], o0 = offsets[e], o1 = offsets[e + 1], m = o1 - o0;
+            if (!(m > 0 && sl >= 0 && sl < pool_slots && o0 >= 0 && o1 <= rows)) continue;
+            const int loc = r - o0, gi = loc / NT, nt = min(NT, m - gi * NT);
             j = loc % NT;
             N = ((T * nt + 7) / 8) * 8;
             BB = b_chunk_bytes(N, NSUB);
-            base = bimg + (size_t)KC * ((size_t)__ldg(boffc + e) + (size_t)gi * b_chunk_bytes(nfull, NSUB));
+            base = bimg + (size_t)KC * ((size_t)boffc[e] + (size_t)gi * b_chunk_bytes(nfull, NSUB));
         }
-        const size_t sr = gather ? (size_t)(__ldg(gather + r) / gk) : (size_t)r;
+        const size_t sr = gather ? (size_t)(gather[r] / gk) : (size_t)r;
         const void* row = IN_F32 ? static_cast<const void*>(static_cast<const float*>(in) + sr * K)
                                  : static_cast<const void*>(static_cast<const uint16_t*>(in) + sr * K);
         int p = 0;

@@ -49,17 +49,17 @@ constexpr int kStatic = 1024;        // bytes of static shared memory at most
 constexpr int kABytes = 128 * 128;   // 128 features x 64 inner indices
 constexpr int kStaging = 8 * 4096;
 
-// Steps of 64 summed in one accumulator where the output is float32.  The
-// tensor core adds to its fp32 accumulator with truncation, so the relative
-// error of a sum grows by about 1e-6 for every 1000 inner indices; partial
-// sums are added up outside it, rounded to nearest.  FWD, DX: of 256 inner
-// indices, in registers (2.4e-7 off, less than fp32 sums by FMAs from 1000
+// Steps of 64 summed in one accumulator.  The tensor core adds to its fp32
+// accumulator with truncation, so the relative error of a sum grows by about
+// 1e-6 for every 1000 inner indices, and by 6e-6 where all terms have one
+// sign (6.6e-3 too small at 2^20); partial sums are added up outside it,
+// rounded to nearest.  float32 outputs: FWD, DX of 256 inner indices, in registers (2.4e-7 off, less than fp32 sums by FMAs from 1000
 // inner indices on; of 512, 4.7e-7 and 0 to 13% faster, 128, 1.5e-7 and
 // 5 to 17% slower; adding them to the output took 474 us instead of 208 where a tile
 // has eight of them).  DW: of 512 rows, in the output (few experts have
-// several).  bf16 outputs round to 2^-9 anyway: one accumulator for the whole
-// sum.
-constexpr int kPartial = 4, kPartialDw = 8;
+// several).  bf16 outputs: of 8192 inner indices, 5e-5 too small at most beside
+// a rounding of 2^-9, so that one accumulator holds the sums of most layers.
+constexpr int kPartial = 4, kPartialDw = 8, kPartialBf16 = 128;
 
 // Registers a thread of the control warps and of the epilogue's where the
 // latter hold 128 float32 sums each: together what the block is launched with,
@@ -266,8 +266,9 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap& out
     }
 }
 
-// SUMS: row products summed up in the epilogue's registers, for float32 outputs
-// and for an inner index split over a cluster.
+// SUMS: row products summed up in the epilogue's registers, for float32 outputs,
+// for an inner index split over a cluster and for more steps than an
+// accumulator takes.
 template <int MODE, int NB, bool SUMS>
 struct Epilogue {
     static constexpr int WARPS = MODE == DW || (SUMS && NB > 32) ? 8 : 4;
@@ -627,7 +628,7 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     a.out = y;
     a.ldo = ldy;
     a.out_f32 = y_dtype == MOE_DT_F32;
-    a.partial = a.out_f32 ? kPartial : 1 << 30;
+    a.partial = a.out_f32 ? kPartial : kPartialBf16;
     a.E = E;
     a.rows = rows;
     a.M = MODE == FWD ? out : in;
@@ -654,14 +655,16 @@ int row_product(int E, int in, int out, const uint16_t* x, int64_t ldx, const ui
     const bool small = rows <= 16 * (int64_t)E || small_tiles <= sms;
     a.box = small ? 16 : 32;
     if (!encode_rows(&tb, E_BF16, x, ldx, a.K, rows, a.box, small ? 32 : 128)) return MOE_ERR_CUDA;
-    a.split = small ? split_of(small_tiles, (a.K + 63) / 64, sms) : 1;
+    const int steps = (a.K + 63) / 64;
+    a.split = small ? split_of(small_tiles, steps, sms) : 1;
+    const bool sums = a.out_f32 || a.split > 1 || steps > a.partial;
     cudaStream_t st = as_stream(stream);
     if (small)
-        return a.out_f32 || a.split > 1 ? launch<MODE, 32, 1, true>(a, small_tiles, sms, dev, ta, tb, ta, st)
-                                        : launch<MODE, 32, 1, false>(a, small_tiles, sms, dev, ta, tb, ta, st);
+        return sums ? launch<MODE, 32, 1, true>(a, small_tiles, sms, dev, ta, tb, ta, st)
+                    : launch<MODE, 32, 1, false>(a, small_tiles, sms, dev, ta, tb, ta, st);
     const int64_t tiles = most_tiles(E, rows, 256, (a.M + 255) / 256);
-    return a.out_f32 ? launch<MODE, 256, 2, true>(a, tiles, sms, dev, ta, tb, ta, st)
-                     : launch<MODE, 256, 2, false>(a, tiles, sms, dev, ta, tb, ta, st);
+    return sums ? launch<MODE, 256, 2, true>(a, tiles, sms, dev, ta, tb, ta, st)
+                : launch<MODE, 256, 2, false>(a, tiles, sms, dev, ta, tb, ta, st);
 }
 
 }  // namespace

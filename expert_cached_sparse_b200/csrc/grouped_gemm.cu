@@ -63,8 +63,8 @@ constexpr int kPartial = 4, kPartialDw = 8, kPartialBf16 = 128;
 
 // Registers a thread of the control warps and of the epilogue's where the
 // latter hold 128 float32 sums each: together what the block is launched with,
-// 128 * 72 + 256 * 216 = 384 * 168.
-constexpr int kRegs = 168, kControlRegs = 72, kSumRegs = 216;
+// 128 * 88 + 256 * 208 = 384 * 168 (72 and 216: DW's control warps spill).
+constexpr int kRegs = 168, kControlRegs = 88, kSumRegs = 208;
 
 enum Mode { FWD, DX, DW };
 
@@ -194,13 +194,19 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi)
     return pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
 }
 
-// Adds 8 (n < 16) or 16 adjacent elements to bf16 ones: fp32 sums, one rounding.
-__device__ __forceinline__ void add_row16(uint16_t* p, const uint32_t (&d)[16], int n)
+// Stores 8 (n < 16) or 16 adjacent elements as bf16, or adds them to what is
+// there: fp32 sums, one rounding.
+__device__ __forceinline__ void store_row16(uint16_t* p, const uint32_t (&d)[16], int n, bool add)
 {
     uint4* o = reinterpret_cast<uint4*>(p);
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         if (j && n < 16) break;   // `in` is a multiple of 8
+        if (!add) {
+            o[j] = make_uint4(pack_bf16(d[8 * j], d[8 * j + 1]), pack_bf16(d[8 * j + 2], d[8 * j + 3]),
+                              pack_bf16(d[8 * j + 4], d[8 * j + 5]), pack_bf16(d[8 * j + 6], d[8 * j + 7]));
+            continue;
+        }
         const uint4 b = o[j];
         uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -208,6 +214,21 @@ __device__ __forceinline__ void add_row16(uint16_t* p, const uint32_t (&d)[16], 
             w[k] = pack_bf16(__uint_as_float(d[8 * j + 2 * k]) + bf16_bits_to_f32(w[k] & 0xFFFFu),
                              __uint_as_float(d[8 * j + 2 * k + 1]) + bf16_bits_to_f32(w[k] >> 16));
         o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Adds n columns of an accumulator, a multiple of 16 of them, to a thread's sums.
+template <int CW>
+__device__ __forceinline__ void add_cols(float (&sum)[CW], uint32_t src, int n)
+{
+#pragma unroll
+    for (int c = 0; c < CW; c += 16) {
+        if (c >= n) break;
+        uint32_t d[16];
+        tmem_ld16(src + c, d);
+        wait_ld(d);
+#pragma unroll
+        for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(d[j]);
     }
 }
 
@@ -274,7 +295,8 @@ struct Epilogue {
     static constexpr int WARPS = MODE == DW || (SUMS && NB > 32) ? 8 : 4;
     static constexpr int THREADS = 128 + 32 * WARPS;
     static constexpr int CW = NB / (WARPS / 4);        // columns of one warp
-    static constexpr bool SPLIT = SUMS && CW > 64;     // registers moved from the control warps
+    // registers moved from the control warps (DW: for bf16 outputs over many rows)
+    static constexpr bool SPLIT = (SUMS || MODE == DW) && CW > 64;
 };
 static_assert(128 * kControlRegs + 256 * kSumRegs <= 384 * kRegs, "a larger split never starts");
 
@@ -480,6 +502,35 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
             const bool none = MODE == DW && v.steps == 0;   // an expert without rows: its gradient is zero
             if (none && a.accumulate) continue;
             const int cw = EPI::CW * ((warp - 4) >> 2), c1 = min(v.n, cw + EPI::CW);
+            if constexpr (MODE == DW) {
+                if (!a.out_f32 && v.steps > a.partial) {   // more rows than a bf16 output's accumulator takes
+                    float sum[EPI::CW];
+#pragma unroll
+                    for (int c = 0; c < EPI::CW; c++) sum[c] = 0.0f;
+                    for (int s = 0; s < v.steps; s += a.partial, it++) {
+                        const int ab = it & 1;
+                        if (!(ok = mbar_wait_warp(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+                        fence_after();
+                        add_cols(sum, tmem + (uint32_t)(ab * NB + cw) + ((uint32_t)(32 * q) << 16), v.n - cw);
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+                    }
+                    if (ok && mine) {
+                        uint16_t* o = static_cast<uint16_t*>(a.out) + ((int64_t)v.e * a.M + f) * a.N + v.c0 + cw;
+#pragma unroll
+                        for (int c = 0; c < EPI::CW; c += 16) {
+                            if (cw + c >= v.n) break;
+                            uint32_t d[16];
+#pragma unroll
+                            for (int j = 0; j < 16; j++) d[j] = __float_as_uint(sum[c + j]);
+                            store_row16(o + c, d, v.n - cw - c, a.accumulate);
+                        }
+                    }
+                    __syncwarp();
+                    continue;
+                }
+            }
             float sum[SUMS ? EPI::CW : 1];
             if (SUMS) {
 #pragma unroll
@@ -502,7 +553,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                             uint32_t d[16];
                             tmem_ld16(src + c, d);
                             wait_ld(d);
-                            if (mine) add_row16(static_cast<uint16_t*>(a.out) + at + c, d, v.n - c);
+                            if (mine) store_row16(static_cast<uint16_t*>(a.out) + at + c, d, v.n - c, true);
                             __syncwarp();   // the warp's next tensor-memory load is a converged one
                         }
                     } else if (v.m0 + 32 * q < a.M) {
@@ -510,15 +561,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                         store_tile(a, tm_out, v, staging + 8192 * q, tile, src, v.m0 + 32 * q, (warp - 4) >> 2, none, add);
                     }
                 } else if constexpr (SUMS) {
-#pragma unroll
-                    for (int c = 0; c < EPI::CW; c += 16) {
-                        if (cw + c >= v.n) break;
-                        uint32_t d[16];
-                        tmem_ld16(src + cw + c, d);
-                        wait_ld(d);
-#pragma unroll
-                        for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(d[j]);
-                    }
+                    add_cols(sum, src + cw, v.n - cw);
                 } else {
                     store_cols(static_cast<uint16_t*>(a.out) + (int64_t)v.c0 * a.ldo + f, a.ldo, src, v.n, mine);
                 }
@@ -765,7 +808,7 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
     a.ldo = in;
     a.out_f32 = dw_dtype == MOE_DT_F32;
     a.accumulate = accumulate ? 1 : 0;
-    a.partial = a.out_f32 ? kPartialDw : 1 << 30;
+    a.partial = a.out_f32 ? kPartialDw : kPartialBf16;
     a.E = experts;
     a.rows = rows;
     a.M = out;

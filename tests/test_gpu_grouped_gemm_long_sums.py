@@ -4,10 +4,10 @@ factors spread the results over a binade, so that bf16 roundings average out ove
 left of the mean relative error is the sums' own.
 
 Bound on that mean: an accumulator takes at most 8192 inner indices, 512 additions of 16 products, each
-off by at most 2^-22 of a running sum that is half the final one on average, 512 * 2^-23 = 2^-14; the sums
-of these partial sums, 128 at 2^20, round to nearest, each off by 2^-25 of a running sum on average and with
-either sign: below 64 * 2^-25 = 2^-19 once half of them go each way.  bf16 rounding is off by at most 2^-8 relative, with standard
-deviation below 2^-8 / sqrt(3), five times which over sqrt(n) bounds its mean."""
+off by at most 2^-22 of a running sum that is half the final one on average, 512 * 2^-23 = 2^-14.  The sums
+of these partial sums, 128 at 2^20 (of float32 outputs 4096 or fewer, with partial sums so much shorter),
+round to nearest, with either sign: below 2^-19.  bf16 rounding is off by at most 2^-8 relative, with
+standard deviation below 2^-8 / sqrt(3), five times which over sqrt(n) bounds its mean."""
 import pytest
 import torch
 
@@ -85,3 +85,23 @@ def test_forward_of_many_experts_with_few_rows():
     y = torch.empty(16 * E, N, dtype=BF, device=DEV)
     A.moe_grouped_gemm(x, w, offsets(*range(16, 16 * E + 1, 16)), y)
     check(y, torch.cat([product64(x[16 * e:16 * e + 16], w[e]) for e in range(E)]))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_weight_gradient(dt, accumulate):
+    """One expert of 2^20 rows between an empty one and a small one."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(53)
+    N, K, small = 136, 392, 300
+    dyt, xt = positive(g, N, LONG + small), positive(g, K, LONG + small)
+    dy, x = dyt.t().contiguous(), xt.t().contiguous()
+    base = 1000 * torch.rand(3, N, K, generator=g, device=DEV)
+    dw = base.to(dt)
+    first = dw.to(F64)
+    A.moe_grouped_gemm_dw(dy, x, offsets(0, LONG, LONG + small), dw, accumulate=accumulate)
+    for e, rows in ((1, slice(0, LONG)), (2, slice(LONG, LONG + small))):
+        ref = product64(dyt[:, rows], xt[:, rows])
+        check(dw[e], ref + first[e] if accumulate else ref)
+    assert torch.equal(dw[0].to(F64), first[0]) if accumulate else not bool(dw[0].any())
+    assert A.moe_get_device_error() == 0

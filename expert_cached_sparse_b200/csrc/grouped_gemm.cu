@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Epilogue<MODE, NB, SUMS>::THREADS, 1)
                     for (int c = 0; c < EPI::CW; c++) sum[c] = 0.0f;
                     for (int s = 0; s < v.steps; s += a.partial, it++) {
                         const int ab = it & 1;
-                        if (!(ok = mbar_wait_warp(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
+                        if (!(ok = mbar_wait_warp<CG>(smem_u32(&acc_full[ab]), (it >> 1) & 1, abort_v, a.wait, err))) break;
                         fence_after();
                         add_cols(sum, tmem + (uint32_t)(ab * NB + cw) + ((uint32_t)(32 * q) << 16), v.n - cw);
                         fence_before();

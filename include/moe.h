@@ -523,10 +523,16 @@ int moe_act_terms(const void* d_x, int32_t x_dtype, int32_t rows, int32_t K, int
  *    leading dimensions of 16-bit and 8-bit ones 16-byte aligned; no output
  *    may overlap an input;
  *  - products are summed in fp32 and rounded once to the output type
- *    (float32 or bf16, nearest even); the tensor core truncates as it adds, so
- *    float32 results are off by about 3e-7 relative (2-norm), weight gradients
- *    of experts with more than 256 rows by up to 5e-7.  The same inputs give
- *    the same bits on every call.  No workspace, nothing read back: every call
+ *    (float32 or bf16, nearest even).  The tensor core truncates as it adds, so
+ *    it takes 256 inner indices at most (weight gradients: 512 rows; e4m3: 128;
+ *    bf16 outputs: 8192), and these partial sums are added one after another,
+ *    rounded to nearest: their roundings grow as the square root of their
+ *    number.  float32 results of normal inputs are off (2-norm, relative) by
+ *    2.4e-7 up to 4096 inner indices, 2.7e-7 at 16384, 6.2e-7 at 2^18; weight
+ *    gradients by 4.8e-7 up to 16384 rows of an expert, 9.6e-7 at 2^20; e4m3
+ *    products by 1e-7 at 16384, 6.8e-7 at 2^18.  bf16 outputs are their
+ *    rounding off, and where all terms have one sign up to 5e-5 too small.
+ *    The same inputs give the same bits on every call.  No workspace, nothing read back: every call
  *    can be captured in a CUDA graph, and calls on different streams may
  *    overlap.
  * Errors: MOE_ERR_INVALID_ARG for bad sizes, types, alignments or NULL
@@ -559,9 +565,9 @@ int moe_grouped_gemm_dx(int32_t experts, int32_t in, int32_t out, const uint16_t
  * the rows r of e of dy[r] x[r]^T.  d_dy [rows][out] bf16 (lddy), d_x
  * [rows][in] bf16 (ldx), d_dw [experts][out][in] in dw_dtype.  accumulate ==
  * 0 stores the sum (zeros for an expert without rows); otherwise it is added
- * to what d_dw holds (in fp32, then rounded to dw_dtype; float32 sums below
- * 2^-126 may become 0), and an expert without rows is left as it was.  rows
- * may be 0.
+ * to what d_dw holds (in fp32, then rounded to dw_dtype), and an expert
+ * without rows is left as it was.  float32 sums below 2^-126 may become 0 with
+ * accumulate, and without for experts of more than 512 rows.  rows may be 0.
  */
 int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, const uint16_t* d_dy, int64_t lddy,
                         const uint16_t* d_x, int64_t ldx, const int32_t* d_offsets, int32_t rows, void* d_dw,

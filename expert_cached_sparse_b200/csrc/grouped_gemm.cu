@@ -771,7 +771,7 @@ extern "C" int moe_grouped_gemm(int32_t experts, int32_t in, int32_t out, const 
     if (int rc = check_gemm_sizes(experts, in, out, rows, 8)) return rc;
     if (!out_dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!d_offsets || !rows_ok(d_x, ldx, in, 2) || !rows_ok(d_w, in, in, 2) || !rows_ok(d_y, ldy, out, dtype_size(y_dtype)))
+    if (!words_ok(d_offsets) || !rows_ok(d_x, ldx, in, 2) || !rows_ok(d_w, in, in, 2) || !rows_ok(d_y, ldy, out, dtype_size(y_dtype)))
         return MOE_ERR_INVALID_ARG;
     return row_product<FWD>(experts, in, out, d_x, ldx, d_w, d_offsets, rows, d_y, ldy, y_dtype, stream);
 }
@@ -783,7 +783,7 @@ extern "C" int moe_grouped_gemm_dx(int32_t experts, int32_t in, int32_t out, con
     if (int rc = check_gemm_sizes(experts, in, out, rows, 8)) return rc;
     if (!out_dtype_ok(dx_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!d_offsets || !rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_w, in, in, 2) ||
+    if (!words_ok(d_offsets) || !rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_w, in, in, 2) ||
         !rows_ok(d_dx, lddx, in, dtype_size(dx_dtype)))
         return MOE_ERR_INVALID_ARG;
     return row_product<DX>(experts, in, out, d_dy, lddy, d_w, d_offsets, rows, d_dx, lddx, dx_dtype, stream);
@@ -794,7 +794,7 @@ extern "C" int moe_grouped_gemm_dw(int32_t experts, int32_t in, int32_t out, con
                                    void* d_dw, int32_t dw_dtype, int32_t accumulate, void* stream)
 {
     if (int rc = check_gemm_sizes(experts, in, out, rows, 8)) return rc;
-    if (!out_dtype_ok(dw_dtype) || !d_offsets || !rows_ok(d_dw, in, in, dtype_size(dw_dtype))) return MOE_ERR_INVALID_ARG;
+    if (!out_dtype_ok(dw_dtype) || !words_ok(d_offsets) || !rows_ok(d_dw, in, in, dtype_size(dw_dtype))) return MOE_ERR_INVALID_ARG;
     if (rows > 0 && (!rows_ok(d_dy, lddy, out, 2) || !rows_ok(d_x, ldx, in, 2))) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = as_stream(stream);
     if (rows == 0) {

@@ -463,7 +463,7 @@ extern "C" int moe_grouped_gemm_fp8(int32_t experts, int32_t in, int32_t out, co
     if (int rc = check_gemm_sizes(experts, in, out, rows, 16)) return rc;
     if (!out_dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (!d_offsets || !d_xs || !d_ws || ((uintptr_t)d_xs & 3) || ((uintptr_t)d_ws & 3) || !rows_ok(d_xq, ldxq, in, 1) ||
+    if (!words_ok(d_offsets) || !words_ok(d_xs) || !words_ok(d_ws) || !rows_ok(d_xq, ldxq, in, 1) ||
         !rows_ok(d_wq, in, in, 1) || !rows_ok(d_y, ldy, out, dtype_size(y_dtype)))
         return MOE_ERR_INVALID_ARG;
     Args a{};

@@ -644,6 +644,8 @@ static inline bool rows_ok(const void* p, int64_t ld, int64_t width, int size)
 {
     return p && !((uintptr_t)p & 15) && ld >= width && ld < ((int64_t)1 << 36) && (ld * size) % 16 == 0;
 }
+// int32 or float32 values.
+static inline bool words_ok(const void* p) { return p && !((uintptr_t)p & 3); }
 static inline bool out_dtype_ok(int t) { return t == MOE_DT_F32 || t == MOE_DT_BF16; }
 static inline int dtype_size(int t) { return t == MOE_DT_F32 ? 4 : 2; }
 

@@ -521,7 +521,8 @@ int moe_act_terms(const void* d_x, int32_t x_dtype, int32_t rows, int32_t K, int
  *  - 1 <= experts <= 4096; in and out are multiples of 8 (moe_grouped_gemm_fp8:
  *    in a multiple of 16) up to 2^20; rows up to 2^30; every matrix and its
  *    leading dimension are multiples of 16 bytes (float32 outputs: ld a
- *    multiple of 4); no output may overlap an input;
+ *    multiple of 4), offsets and scales whole words; no output may overlap an
+ *    input;
  *  - products are summed in fp32 and rounded once to the output type
  *    (float32 or bf16, nearest even).  The tensor core truncates as it adds, so
  *    it takes 256 inner indices at most (weight gradients: 512 rows; e4m3: 128;

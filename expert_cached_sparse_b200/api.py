@@ -427,7 +427,8 @@ def moe_fp8_quantize_weight(w, q, s, stream=None):
 
 # ------------------------------------------------------------------ testing hooks
 def moe_test_set_wait(cycles: int, withhold: bool = False) -> None:
-    """Bounded-wait limit (SM cycles, 0 = default) and stage withholding of later FFN launches."""
+    """Bounded-wait limit (SM cycles, 0 = default) and stage withholding of later launches of the grouped
+    FFN and of the expert products."""
     check("moe_test_set_wait", L.lib.moe_test_set_wait(int(cycles), 1 if withhold else 0))
 
 

@@ -513,7 +513,10 @@ int moe_act_terms(const void* d_x, int32_t x_dtype, int32_t rows, int32_t K, int
  *    expert e owns rows [offsets[e], offsets[e+1]) of the row matrices, any
  *    number of them, none included.  A range that is decreasing or does not
  *    lie inside [0, rows) counts as empty.  Rows that no expert owns are
- *    neither read into a result nor written: they keep what they held;
+ *    neither read into a result nor written: they keep what they held.  (Where
+ *    ranges share rows, weight gradients are those of the ranges, and an element
+ *    of a shared row of y or dx is one of the experts'; if the ranges' rows,
+ *    cut into blocks, come to 2^31 blocks, y or dx is left as it was.)
  *  - row matrices have a leading dimension in elements (ld >= width), so a
  *    column slice of a wider matrix is used in place; weights are packed
  *    [experts][out][in] row-major (the canonical layout of moe_pack_expert:
@@ -638,18 +641,19 @@ int moe_profile_read(moe_prof_entry* h_out, int count, int reset);
 /*
  * First error recorded by a device-side bounded wait since the last clear
  * (MOE_ERR_TIMEOUT when a kernel gave up waiting and drained instead of
- * hanging), 0 if none; clear != 0 resets it.  Synchronous.  The grouped FFN
- * results of a call that timed out, and of FP4 decode calls made while the
- * error is set (their grid barriers give up at once), are undefined; clear
- * the error before relying on results again.
+ * hanging), 0 if none; clear != 0 resets it.  Synchronous.  What a grouped FFN
+ * call or an expert product that timed out wrote, and what FP4 decode calls
+ * made while the error is set (their grid barriers give up at once) write, is
+ * undefined; clear the error before relying on results again.
  */
 int moe_get_device_error(int clear);
 
 /*
- * Testing hook, process-wide, for grouped-FFN launches made afterwards:
+ * Testing hook, process-wide, for launches of the grouped FFN and of the
+ * expert products made afterwards:
  * `cycles` > 0 sets the limit of the kernels' bounded waits to that many SM
  * clock cycles (0 restores the default of about 2 s), and withhold != 0
- * makes the first CTA's copy issuer leave its first ring stage unfilled, so
+ * makes the first CTA's copy issuers leave their first ring stage unfilled, so
  * that the wait for it runs out: the kernel records MOE_ERR_TIMEOUT, lets
  * its own copies and MMAs finish and returns.  Drains of a CTA's own
  * asynchronous work keep the default limit.  MOE_ERR_INVALID_ARG for

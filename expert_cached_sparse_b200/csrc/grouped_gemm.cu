@@ -53,12 +53,13 @@ constexpr int kStaging = 8 * 4096;
 // accumulator with truncation, so the relative error of a sum grows by about
 // 1e-6 for every 1000 inner indices, and by 6e-6 where all terms have one
 // sign (6.6e-3 too small at 2^20); partial sums are added up outside it,
-// rounded to nearest.  float32 outputs: FWD, DX of 256 inner indices, in registers (2.4e-7 off, less than fp32 sums by FMAs from 1000
-// inner indices on; of 512, 4.7e-7 and 0 to 13% faster, 128, 1.5e-7 and
-// 5 to 17% slower; adding them to the output took 474 us instead of 208 where a tile
-// has eight of them).  DW: of 512 rows, in the output (few experts have
-// several).  bf16 outputs: of 8192 inner indices, 5e-5 too small at most beside
-// a rounding of 2^-9, so that one accumulator holds the sums of most layers.
+// rounded to nearest.  float32 outputs: FWD, DX of 256 inner indices, in
+// registers (2.4e-7 off, less than fp32 sums by FMAs from 1000 inner indices
+// on; of 512, 4.7e-7 and 0 to 13% faster, 128, 1.5e-7 and 5 to 17% slower;
+// adding them to the output took 474 us instead of 208 where a tile has eight
+// of them).  DW: of 512 rows, in the output (few experts have several).  bf16
+// outputs: of 8192 inner indices, 5e-5 too small at most beside a rounding of
+// 2^-9, so that one accumulator holds the sums of most layers.
 constexpr int kPartial = 4, kPartialDw = 8, kPartialBf16 = 128;
 
 // Registers a thread of the control warps and of the epilogue's where the
